@@ -347,6 +347,109 @@ CLHA_API clha_status clha_quantize_as(clha_ctx* ctx, clha_factor_form form, cons
 CLHA_API clha_status clha_loss(clha_ctx* ctx, const void* W, clha_dtype dtype, const float* W_hat,
                       const float* H, int n_h, int batch, int d_out, int d_in, double* loss_out);
 
+/* ------------------------------------------------------------------------------ 4-bit expert layer */
+
+/* The layer that the quantized experts run in, in microscaled 4-bit floating point:
+ *   clha_route_gated -> clha_gather (perm only) -> clha_fp4_quantize (the routed rows)
+ *   -> clha_fp4_expert_act -> clha_fp4_quantize -> clha_fp4_matmul -> clha_combine.
+ * The pages stop at the quantized weights; these calls have no counterpart there. Nothing in them
+ * synchronises, allocates or uses the context's workspace, so calls of several streams' contexts may
+ * overlap and every call may be captured into a graph; results do not depend on timing. */
+
+typedef enum { CLHA_SCORE_SOFTMAX = 0, CLHA_SCORE_SIGMOID = 1 } clha_score;
+typedef enum { CLHA_GROUP_MAX = 0, CLHA_GROUP_TOP2 = 1 } clha_group_rank;
+/* E experts in n_groups equal groups (1: no groups) of which the first top_groups stay, the groups
+ * ranked by their largest choice or by the sum of their two largest (of one, where a group has one
+ * expert); k experts a token; weights divided by their sum where renormalise is nonzero, then times
+ * scale. 1 <= k <= E * top_groups / n_groups, E <= 1024, n_groups divides E. */
+typedef struct {
+    int E, k;
+    int score;                 /* clha_score */
+    int n_groups, top_groups;
+    int group_rank;            /* clha_group_rank */
+    int renormalise;
+    float scale;
+} clha_route_params;
+
+/* Top-k routing with gate weights. For each of n tokens, of its router logits l [n, E] (f32 or bf16): the
+ * scores s = softmax(l) or sigmoid(l), the choices c = s + bias (bias: float32 [E] or NULL), and the k
+ * experts of the largest choices, in descending order, ties to the lower expert (and group). ids [n, k]
+ * int32 are the experts, weights [n, k] float32 their scores (without the bias; 1/k each if renormalised
+ * scores are all zero), counts [E] int32 is OVERWRITTEN with the tokens of each expert. Choices are
+ * compared as float64 values, whatever the kernel computes them in; without a bias the logits decide,
+ * unless groups are ranked by sums. A NaN or Inf logit or bias is recorded as CLHA_ERR_NONFINITE (and
+ * counts as 0, so the ids stay in range). */
+CLHA_API clha_status clha_route_gated(clha_ctx* ctx, const void* logits, clha_dtype dtype, int64_t n,
+                                      const clha_route_params* params, const float* bias, int32_t* ids,
+                                      float* weights, int32_t* counts);
+
+/* Microscaled 4-bit floating point. A row of d values (d a multiple of 128) is cut into blocks; a block
+ * shares one 8-bit scale s, and each value is a 4-bit e2m1 code (+-0, 0.5, 1, 1.5, 2, 3, 4, 6) that stands
+ * for q * s * g, g being the float32 scale of the matrix (1 where tensor_scale is NULL).
+ *   CLHA_FP4_E8M0_32  blocks of 32, s a power of two: s = 2^(floor(log2(max|x| / g)) - 2)
+ *   CLHA_FP4_E4M3_16  blocks of 16, s an e4m3 number: max|x| / (6 g) rounded to nearest, at least 2^-9 and
+ *                     at most 448 (0 for a block of zeros)
+ * q is x / (s g) rounded to nearest, ties to the even code, saturating at +-6; a value that rounds to
+ * zero keeps its sign. All of it is decided as in exact arithmetic.
+ * codes: uint8 [rows, d / 2], the even column in the low four bits. scales: uint8, tiles of 128 rows x 4
+ * blocks of 512 bytes each, tiles row-major (rows rounded up to 128): row r, block b of a tile at byte
+ * 16 (r % 32) + 4 (r / 32) + b; scales of rows past the end are 0. clha_fp4_scale_bytes gives their size
+ * (-1 for a bad format, rows < 0 or d not a positive multiple of 128). codes and scales of the calls
+ * below are 16-byte aligned. */
+typedef enum { CLHA_FP4_E8M0_32 = 0, CLHA_FP4_E4M3_16 = 1 } clha_fp4_format;
+CLHA_API int64_t clha_fp4_scale_bytes(clha_fp4_format format, int64_t rows, int d);
+
+/* Matrix scales of `batch` matrices X [batch, rows, d] (f32 or bf16): scale [batch] (device float32) is
+ * max|x| over the largest number that the format's blocks reach under scale 1 (6 for E8M0_32, 6 * 448 for
+ * E4M3_16); 1 for a matrix of zeros. A NaN or Inf entry is recorded as CLHA_ERR_NONFINITE. */
+CLHA_API clha_status clha_fp4_tensor_scale(clha_ctx* ctx, const void* X, clha_dtype dtype, int batch, int64_t rows,
+                                           int d, clha_fp4_format format, float* scale);
+
+/* Quantizes `rows` rows to codes and scales. With perm NULL row r is X[r] (and rows == n); with perm
+ * (int32 [rows], as clha_gather writes it) it is X[perm[r]], zeros where perm is negative: the routed
+ * rows go straight into their segments. With seg (clha_gather's, int64 [2E + 1]) only rows below seg[E]
+ * are written; without it E is ignored. tensor_scale: device float32 [n_scales], each for an equal share
+ * of the rows (n_scales divides rows; 1 for one matrix), or NULL. A block with a NaN or Inf gets the
+ * format's NaN scale (0xff or 0x7f) and zero codes, and is recorded as CLHA_ERR_NONFINITE; a perm entry
+ * >= n or a tensor scale that is not positive and finite is recorded as CLHA_ERR_INVALID_ARG. */
+CLHA_API clha_status clha_fp4_quantize(clha_ctx* ctx, const void* X, clha_dtype dtype, int64_t n, int d,
+                                       const int32_t* perm, int64_t rows, const int64_t* seg, int E,
+                                       clha_fp4_format format, const float* tensor_scale, int64_t n_scales,
+                                       uint8_t* codes, uint8_t* scales);
+/* The values q s g of codes and scales, [rows, d] f32 or bf16, rounded once. The f32 values of a weight
+ * are a W_hat for clha_loss. */
+CLHA_API clha_status clha_fp4_dequantize(clha_ctx* ctx, const uint8_t* codes, const uint8_t* scales, int64_t rows,
+                                         int d, clha_fp4_format format, const float* tensor_scale, int64_t n_scales,
+                                         void* X_hat, clha_dtype dtype);
+
+/* Y [rows, d_out] (f32 or bf16) = X W^T of operands in the same format: X [rows, d_in], W [E, d_out, d_in],
+ * d_in and d_out multiples of 128, sums in float32 on the tensor cores. With seg NULL, E is 1; with seg,
+ * rows follow its segments (rows >= seg[E]; segments start at multiples of 128) and expert e's rows meet W[e]:
+ * rows of a segment behind its tokens are written as zero, rows from seg[E] on are left as they were.
+ * x_scale: device float32 [1], w_scale [E], or NULL. rows * d_in and E * d_out * d_in below 2^37,
+ * rows and E * d_out below 2^31. Y is 16-byte aligned. */
+CLHA_API clha_status clha_fp4_matmul(clha_ctx* ctx, clha_fp4_format format, const uint8_t* x_codes,
+                                     const uint8_t* x_scales, const float* x_scale, int64_t rows, int d_in,
+                                     const int64_t* seg, int E, const uint8_t* w_codes, const uint8_t* w_scales,
+                                     const float* w_scale, int d_out, void* Y, clha_dtype y_dtype);
+/* clha_expert_act on 4-bit operands: h [rows, d_ff] bf16 = SiLU(x Wg^T) * (x Wu^T), Wg and Wu [E, d_ff, d_model];
+ * the float32 sums' product is rounded once. Arguments as in clha_fp4_matmul. */
+CLHA_API clha_status clha_fp4_expert_act(clha_ctx* ctx, clha_fp4_format format, const uint8_t* x_codes,
+                                         const uint8_t* x_scales, const float* x_scale, int64_t rows, int d_model,
+                                         const int64_t* seg, int E, const uint8_t* g_codes, const uint8_t* g_scales,
+                                         const float* g_scale, const uint8_t* u_codes, const uint8_t* u_scales,
+                                         const float* u_scale, int d_ff, void* h);
+
+/* Y[t] = add[t] + sum_j weights[t, j] Z[row of token t in the segment of expert ids[t, j]], j ascending, in
+ * float32, for n tokens (n < 2^31). Z [rows, d] (f32 or bf16) is in the segment layout of perm and seg, which
+ * clha_gather wrote for these ids; weights float32 [n, k] (NULL: all 1); add [n, d] of Y's type, or NULL; it
+ * may be Y itself. A slot whose token is not in its expert's segment is recorded as CLHA_ERR_INVALID_ARG
+ * and adds nothing. d a multiple of 128; Z, add and Y 16-byte aligned. */
+CLHA_API clha_status clha_combine(clha_ctx* ctx, const void* Z, clha_dtype z_dtype, int64_t rows, int d,
+                                  const int32_t* ids, const float* weights, int64_t n, int k, int E,
+                                  const int64_t* seg, const int32_t* perm, const void* add, void* Y,
+                                  clha_dtype y_dtype);
+
 /* ------------------------------------------------------------------------------ analysis */
 
 #define CLHA_DIVERGENCE_MAX_LAYERS 1024

@@ -36,10 +36,21 @@ SYMBOLS = [
     "clha_collect_gathered", "clha_expert_act_gathered", "clha_set_act_kernel", "clha_last_act_kernel",
     "clha_set_factor_wait_limit", "clha_pack_upper", "clha_unpack_upper", "clha_factor_groups_as",
     "clha_quantize_as",
+    "clha_route_gated", "clha_fp4_scale_bytes", "clha_fp4_tensor_scale", "clha_fp4_quantize", "clha_fp4_dequantize",
+    "clha_fp4_matmul", "clha_fp4_expert_act", "clha_combine",
 ]
 FACTOR_MAX_GROUPS = 4
 # clha_factor_form: U with H_d^-1 = U^T U, or F, the block-scaled Cholesky factor of H_d (GPTQ only)
 FACTOR_INV_CHOL, FACTOR_BLOCK_CHOL = 0, 1
+
+SCORE_SOFTMAX, SCORE_SIGMOID = 0, 1          # clha_score
+GROUP_MAX, GROUP_TOP2 = 0, 1                 # clha_group_rank
+FP4_E8M0_32, FP4_E4M3_16 = 0, 1              # clha_fp4_format
+
+
+class RouteParams(C.Structure):
+    _fields_ = [("E", C.c_int), ("k", C.c_int), ("score", C.c_int), ("n_groups", C.c_int), ("top_groups", C.c_int),
+                ("group_rank", C.c_int), ("renormalise", C.c_int), ("scale", C.c_float)]
 
 
 class FactorGroup(C.Structure):
@@ -110,6 +121,14 @@ def load(path: str = LIB_PATH):
         "clha_set_factor_wait_limit": (i32, [vp, C.c_uint64]),
         "clha_pack_upper": (i32, [vp, vp, i64, i64, i64, i32, vp]),
         "clha_unpack_upper": (i32, [vp, vp, i64, i64, i64, i32, vp]),
+        "clha_route_gated": (i32, [vp, vp, i32, i64, C.POINTER(RouteParams), vp, vp, vp, vp]),
+        "clha_fp4_scale_bytes": (i64, [i32, i64, i32]),
+        "clha_fp4_tensor_scale": (i32, [vp, vp, i32, i32, i64, i32, i32, vp]),
+        "clha_fp4_quantize": (i32, [vp, vp, i32, i64, i32, vp, i64, vp, i32, i32, vp, i64, vp, vp]),
+        "clha_fp4_dequantize": (i32, [vp, vp, vp, i64, i32, i32, vp, i64, vp, i32]),
+        "clha_fp4_matmul": (i32, [vp, i32, vp, vp, vp, i64, i32, vp, i32, vp, vp, vp, i32, vp, i32]),
+        "clha_fp4_expert_act": (i32, [vp, i32, vp, vp, vp, i64, i32, vp, i32, vp, vp, vp, vp, vp, vp, i32, vp]),
+        "clha_combine": (i32, [vp, vp, i32, i64, i32, vp, vp, i64, i32, i32, vp, vp, vp, vp, i32]),
     }
     for name, (res, args) in sig.items():
         fn = getattr(lib, name)
@@ -398,3 +417,110 @@ def clha_unpack_upper(ctx: Context, packed, n_outer: int, outer_stride: int, n_i
     """The inverse of clha_pack_upper on the upper triangles (the strict lower ones are left alone)."""
     ctx._check(load().clha_unpack_upper(ctx.handle, _p(packed), n_outer, outer_stride, n_inner, d,
                                         _mat_ptr(S, first, n_outer, outer_stride, n_inner, d)))
+
+
+def _check_sizes(call: str, **want):
+    """Refuses a tensor with fewer elements than the call would read or write: name=(tensor, elements)."""
+    for name, (t, numel) in want.items():
+        if t is not None and t.numel() < numel:
+            raise ValueError(f"{call}: {name} has {t.numel()} elements, needs {numel}")
+
+
+def _check_types(call: str, **want):
+    """Refuses a tensor of another element type: name=(tensor, dtype)."""
+    for name, (t, dtype) in want.items():
+        if t is not None and t.dtype != dtype:
+            raise TypeError(f"{call}: {name} is {t.dtype}, needs {dtype}")
+
+
+def clha_route_gated(ctx: Context, logits, n: int, E: int, k: int, ids, weights, counts, score: int = SCORE_SOFTMAX,
+                     bias=None, n_groups: int = 1, top_groups: int = 1, group_rank: int = GROUP_MAX,
+                     renormalise: bool = True, scale: float = 1.0):
+    """Top-k routing with gate weights: ids int32 [n, k], weights float32 [n, k], counts int32 [E]; logits
+    [n, E] float32 or bfloat16, bias float32 [E] or None (added for the choice only)."""
+    _check_sizes("clha_route_gated", logits=(logits, n * E), ids=(ids, n * k), weights=(weights, n * k),
+                 counts=(counts, E), bias=(bias, E))
+    _check_types("clha_route_gated", ids=(ids, torch.int32), weights=(weights, torch.float32),
+                 counts=(counts, torch.int32), bias=(bias, torch.float32))
+    rp = RouteParams(E, k, score, n_groups, top_groups, group_rank, int(renormalise), scale)
+    ctx._check(load().clha_route_gated(ctx.handle, _p(logits), _dtype(logits), n, C.byref(rp), _p(bias), _p(ids),
+                                       _p(weights), _p(counts)))
+
+
+def clha_fp4_scale_bytes(fmt: int, rows: int, d: int) -> int:
+    """Bytes of the tiled scales of [rows, d] (-1 for a bad format or size)."""
+    return load().clha_fp4_scale_bytes(fmt, rows, d)
+
+
+def clha_fp4_tensor_scale(ctx: Context, X, batch: int, rows: int, d: int, fmt: int, scale):
+    """scale (float32 [batch]) of the matrices X [batch, rows, d]: max|x| over the format's largest number."""
+    _check_sizes("clha_fp4_tensor_scale", X=(X, batch * rows * d), scale=(scale, batch))
+    _check_types("clha_fp4_tensor_scale", scale=(scale, torch.float32))
+    ctx._check(load().clha_fp4_tensor_scale(ctx.handle, _p(X), _dtype(X), batch, rows, d, fmt, _p(scale)))
+
+
+def _fp4_sizes(call: str, fmt: int, rows: int, d: int, codes, scales, tensor_scale=None):
+    """Checks of one operand's buffers: codes [rows, d / 2], the tiled scales, float32 matrix scales."""
+    _check_types(call, codes=(codes, torch.uint8), scales=(scales, torch.uint8),
+                 tensor_scale=(tensor_scale, torch.float32))
+    _check_sizes(call, codes=(codes, rows * d // 2), scales=(scales, load().clha_fp4_scale_bytes(fmt, rows, d)))
+
+
+def clha_fp4_quantize(ctx: Context, X, n: int, d: int, fmt: int, codes, scales, tensor_scale=None, perm=None,
+                      rows: int | None = None, seg=None, E: int = 1):
+    """codes uint8 [rows, d / 2] and tiled scales (clha_fp4_scale_bytes) of X [n, d], or, with perm (int32 [rows]),
+    of the rows X[perm[r]] (zeros where negative), below seg[E] only if seg is given. tensor_scale: float32,
+    each entry for an equal share of the rows."""
+    rows = n if rows is None else rows
+    _fp4_sizes("clha_fp4_quantize", fmt, rows, d, codes, scales, tensor_scale)
+    _check_sizes("clha_fp4_quantize", X=(X, n * d), perm=(perm, rows), seg=(seg, 2 * E + 1))
+    _check_types("clha_fp4_quantize", perm=(perm, torch.int32), seg=(seg, torch.int64))
+    ctx._check(load().clha_fp4_quantize(ctx.handle, _p(X), _dtype(X), n, d, _p(perm), rows, _p(seg), E, fmt,
+                                        _p(tensor_scale), 0 if tensor_scale is None else tensor_scale.numel(), _p(codes),
+                                        _p(scales)))
+
+
+def clha_fp4_dequantize(ctx: Context, codes, scales, rows: int, d: int, fmt: int, X_hat, tensor_scale=None):
+    """X_hat [rows, d] (float32 or bfloat16) = the values that codes and scales stand for."""
+    _fp4_sizes("clha_fp4_dequantize", fmt, rows, d, codes, scales, tensor_scale)
+    _check_sizes("clha_fp4_dequantize", X_hat=(X_hat, rows * d))
+    ctx._check(load().clha_fp4_dequantize(ctx.handle, _p(codes), _p(scales), rows, d, fmt, _p(tensor_scale),
+                                          0 if tensor_scale is None else tensor_scale.numel(), _p(X_hat),
+                                          _dtype(X_hat)))
+
+
+def clha_fp4_matmul(ctx: Context, fmt: int, x_codes, x_scales, rows: int, d_in: int, w_codes, w_scales, d_out: int, Y,
+                    x_scale=None, w_scale=None, seg=None, E: int = 1):
+    """Y [rows, d_out] (float32 or bfloat16) = X W^T of 4-bit operands; with seg, expert e's segment meets W[e]
+    of w_codes [E, d_out, d_in / 2]. x_scale float32 [1], w_scale float32 [E]."""
+    _fp4_sizes("clha_fp4_matmul", fmt, rows, d_in, x_codes, x_scales, x_scale)
+    _fp4_sizes("clha_fp4_matmul", fmt, E * d_out, d_in, w_codes, w_scales, w_scale)
+    _check_sizes("clha_fp4_matmul", Y=(Y, rows * d_out), seg=(seg, 2 * E + 1), x_scale=(x_scale, 1), w_scale=(w_scale, E))
+    _check_types("clha_fp4_matmul", seg=(seg, torch.int64))
+    ctx._check(load().clha_fp4_matmul(ctx.handle, fmt, _p(x_codes), _p(x_scales), _p(x_scale), rows, d_in, _p(seg), E,
+                                      _p(w_codes), _p(w_scales), _p(w_scale), d_out, _p(Y), _dtype(Y)))
+
+
+def clha_fp4_expert_act(ctx: Context, fmt: int, x_codes, x_scales, rows: int, d_model: int, g_codes, g_scales, u_codes,
+                        u_scales, d_ff: int, h, x_scale=None, g_scale=None, u_scale=None, seg=None, E: int = 1):
+    """h [rows, d_ff] bfloat16 = SiLU(X Wg^T) * (X Wu^T) of 4-bit operands; arguments as clha_fp4_matmul's."""
+    call = "clha_fp4_expert_act"
+    _fp4_sizes(call, fmt, rows, d_model, x_codes, x_scales, x_scale)
+    _fp4_sizes(call, fmt, E * d_ff, d_model, g_codes, g_scales, g_scale)
+    _fp4_sizes(call, fmt, E * d_ff, d_model, u_codes, u_scales, u_scale)
+    _check_sizes(call, h=(h, rows * d_ff), seg=(seg, 2 * E + 1), x_scale=(x_scale, 1), g_scale=(g_scale, E),
+                 u_scale=(u_scale, E))
+    _check_types(call, seg=(seg, torch.int64), h=(h, torch.bfloat16))
+    ctx._check(load().clha_fp4_expert_act(ctx.handle, fmt, _p(x_codes), _p(x_scales), _p(x_scale), rows, d_model,
+                                          _p(seg), E, _p(g_codes), _p(g_scales), _p(g_scale), _p(u_codes), _p(u_scales),
+                                          _p(u_scale), d_ff, _p(h)))
+
+
+def clha_combine(ctx: Context, Z, rows: int, d: int, ids, weights, n: int, k: int, E: int, seg, perm, Y, add=None):
+    """Y [n, d] = add + sum_j weights[:, j] * (the row of Z that holds the token in expert ids[:, j]'s segment)."""
+    _check_sizes("clha_combine", Z=(Z, rows * d), ids=(ids, n * k), weights=(weights, n * k), seg=(seg, 2 * E + 1),
+                 perm=(perm, rows), Y=(Y, n * d), add=(add, n * d))
+    _check_types("clha_combine", ids=(ids, torch.int32), weights=(weights, torch.float32), seg=(seg, torch.int64),
+                 perm=(perm, torch.int32), add=(add, Y.dtype))
+    ctx._check(load().clha_combine(ctx.handle, _p(Z), _dtype(Z), rows, d, _p(ids), _p(weights), n, k, E, _p(seg),
+                                   _p(perm), _p(add), _p(Y), _dtype(Y)))

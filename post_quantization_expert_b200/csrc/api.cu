@@ -98,6 +98,10 @@ static const char* kernel_name(int kid) {
         case KID_QUANTIZE: return "clha_quantize";
         case KID_LOSS: return "clha_loss";
         case KID_DIVERGENCE: return "clha_routing_divergence";
+        case KID_GATE: return "clha_route_gated";
+        case KID_FP4: return "clha_fp4_quantize";
+        case KID_FP4_MATMUL: return "clha_fp4_matmul";
+        case KID_COMBINE: return "clha_combine";
         default: return "kernel";
     }
 }
@@ -670,5 +674,173 @@ extern "C" clha_status clha_unpack_upper(clha_ctx* ctx, const float* packed, int
     SET_DEVICE(ctx);
     LaunchScope launch_scope(ctx);
     CUDA_TRY(launch_unpack_upper(ctx->stream, packed, n_outer, outer_stride, n_inner, d, S), "clha_unpack_upper");
+    return CLHA_OK;
+}
+
+// ------------------------------------------------------------------------------ 4-bit expert layer
+static bool aligned16(const void* p) { return ((uintptr_t)p & 15) == 0; }
+static int fp4_block(clha_fp4_format f) { return f == CLHA_FP4_E8M0_32 ? 32 : f == CLHA_FP4_E4M3_16 ? 16 : 0; }
+
+extern "C" clha_status clha_route_gated(clha_ctx* ctx, const void* logits, clha_dtype dtype, int64_t n,
+                                        const clha_route_params* rp, const float* bias, int32_t* ids, float* weights,
+                                        int32_t* counts) {
+    CHECK_CTX(ctx);
+    REQUIRE(rp, CLHA_ERR_INVALID_ARG, "clha_route_gated: null params");
+    REQUIRE(dtype_size(dtype), CLHA_ERR_INVALID_ARG, "clha_route_gated: unknown dtype");
+    REQUIRE(n >= 0, CLHA_ERR_INVALID_ARG, "clha_route_gated: n < 0");
+    REQUIRE(rp->E >= 1 && rp->E <= 1024, CLHA_ERR_INVALID_ARG, "clha_route_gated: E must be in 1..1024");
+    REQUIRE(rp->score == CLHA_SCORE_SOFTMAX || rp->score == CLHA_SCORE_SIGMOID, CLHA_ERR_INVALID_ARG,
+            "clha_route_gated: unknown score");
+    REQUIRE(rp->group_rank == CLHA_GROUP_MAX || rp->group_rank == CLHA_GROUP_TOP2, CLHA_ERR_INVALID_ARG,
+            "clha_route_gated: unknown group rank");
+    REQUIRE(rp->n_groups >= 1 && rp->E % rp->n_groups == 0 && rp->top_groups >= 1 && rp->top_groups <= rp->n_groups,
+            CLHA_ERR_INVALID_ARG, "clha_route_gated: need n_groups dividing E and 1 <= top_groups <= n_groups");
+    REQUIRE(rp->k >= 1 && rp->k <= rp->E / rp->n_groups * rp->top_groups, CLHA_ERR_INVALID_ARG,
+            "clha_route_gated: k must be in 1..%d, the experts of top_groups groups", rp->E / rp->n_groups * rp->top_groups);
+    REQUIRE(rp->scale == rp->scale && rp->scale - rp->scale == 0.f, CLHA_ERR_INVALID_ARG,
+            "clha_route_gated: scale must be finite");
+    REQUIRE(counts && (n == 0 || (logits && ids && weights)), CLHA_ERR_INVALID_ARG, "clha_route_gated: null pointer");
+    SET_DEVICE(ctx);
+    LaunchScope launch_scope(ctx);
+    CUDA_TRY(launch_route_gated(ctx->stream, ctx->num_sms, logits, dtype == CLHA_F32, n, *rp, bias, ids, weights, counts,
+                                ctx->d_err),
+             "clha_route_gated");
+    return CLHA_OK;
+}
+
+extern "C" int64_t clha_fp4_scale_bytes(clha_fp4_format format, int64_t rows, int d) {
+    const int block = fp4_block(format);
+    if (!block || rows < 0 || d <= 0 || d % 128) return -1;
+    return (rows + 127) / 128 * 128 * (int64_t)(d / block);
+}
+
+extern "C" clha_status clha_fp4_tensor_scale(clha_ctx* ctx, const void* X, clha_dtype dtype, int batch, int64_t rows,
+                                             int d, clha_fp4_format format, float* scale) {
+    CHECK_CTX(ctx);
+    REQUIRE(dtype_size(dtype) && fp4_block(format), CLHA_ERR_INVALID_ARG, "clha_fp4_tensor_scale: unknown dtype or format");
+    REQUIRE(batch >= 1 && batch <= 65535 && rows >= 0, CLHA_ERR_INVALID_ARG,
+            "clha_fp4_tensor_scale: need 1 <= batch <= 65535 and rows >= 0");
+    REQUIRE(d > 0 && d % 128 == 0, CLHA_ERR_UNSUPPORTED_SHAPE, "clha_fp4_tensor_scale: d=%d is not a multiple of 128", d);
+    REQUIRE(scale && (rows == 0 || X) && aligned16(X), CLHA_ERR_INVALID_ARG,
+            "clha_fp4_tensor_scale: null pointer, or X not 16-byte aligned");
+    SET_DEVICE(ctx);
+    LaunchScope launch_scope(ctx);
+    CUDA_TRY(launch_fp4_tensor_scale(ctx->stream, ctx->num_sms, X, dtype == CLHA_F32, batch, rows * d, fp4_block(format),
+                                     scale, ctx->d_err),
+             "clha_fp4_tensor_scale");
+    return CLHA_OK;
+}
+
+extern "C" clha_status clha_fp4_quantize(clha_ctx* ctx, const void* X, clha_dtype dtype, int64_t n, int d,
+                                         const int32_t* perm, int64_t rows, const int64_t* seg, int E,
+                                         clha_fp4_format format, const float* tensor_scale, int64_t n_scales,
+                                         uint8_t* codes, uint8_t* scales) {
+    CHECK_CTX(ctx);
+    REQUIRE(dtype_size(dtype) && fp4_block(format), CLHA_ERR_INVALID_ARG, "clha_fp4_quantize: unknown dtype or format");
+    REQUIRE(n >= 0 && rows >= 0 && (perm || rows == n), CLHA_ERR_INVALID_ARG,
+            "clha_fp4_quantize: need n, rows >= 0, and rows == n without a perm");
+    REQUIRE(!seg || (E >= 1 && E <= 1024), CLHA_ERR_INVALID_ARG, "clha_fp4_quantize: E must be in 1..1024");
+    REQUIRE(d > 0 && d % 128 == 0, CLHA_ERR_UNSUPPORTED_SHAPE, "clha_fp4_quantize: d=%d is not a multiple of 128", d);
+    REQUIRE(!tensor_scale || (n_scales >= 1 && rows % n_scales == 0), CLHA_ERR_INVALID_ARG,
+            "clha_fp4_quantize: n_scales=%lld does not divide rows=%lld", (long long)n_scales, (long long)rows);
+    if (rows == 0) return CLHA_OK;
+    REQUIRE(codes && scales && (n == 0 || X), CLHA_ERR_INVALID_ARG, "clha_fp4_quantize: null pointer");
+    REQUIRE(aligned16(X) && aligned16(codes) && aligned16(scales), CLHA_ERR_INVALID_ARG,
+            "clha_fp4_quantize: X, codes and scales must be 16-byte aligned");
+    SET_DEVICE(ctx);
+    LaunchScope launch_scope(ctx);
+    CUDA_TRY(launch_fp4_quantize(ctx->stream, ctx->num_sms, X, dtype == CLHA_F32, n, d, perm, rows, seg, E,
+                                 fp4_block(format), tensor_scale, tensor_scale ? rows / n_scales : 1, codes, scales,
+                                 ctx->d_err),
+             "clha_fp4_quantize");
+    return CLHA_OK;
+}
+
+extern "C" clha_status clha_fp4_dequantize(clha_ctx* ctx, const uint8_t* codes, const uint8_t* scales, int64_t rows,
+                                           int d, clha_fp4_format format, const float* tensor_scale, int64_t n_scales,
+                                           void* X_hat, clha_dtype dtype) {
+    CHECK_CTX(ctx);
+    REQUIRE(dtype_size(dtype) && fp4_block(format), CLHA_ERR_INVALID_ARG,
+            "clha_fp4_dequantize: unknown dtype or format");
+    REQUIRE(rows >= 0, CLHA_ERR_INVALID_ARG, "clha_fp4_dequantize: rows < 0");
+    REQUIRE(d > 0 && d % 128 == 0, CLHA_ERR_UNSUPPORTED_SHAPE, "clha_fp4_dequantize: d=%d is not a multiple of 128", d);
+    REQUIRE(!tensor_scale || (n_scales >= 1 && rows % n_scales == 0), CLHA_ERR_INVALID_ARG,
+            "clha_fp4_dequantize: n_scales=%lld does not divide rows=%lld", (long long)n_scales, (long long)rows);
+    if (rows == 0) return CLHA_OK;
+    REQUIRE(codes && scales && X_hat, CLHA_ERR_INVALID_ARG, "clha_fp4_dequantize: null pointer");
+    REQUIRE(aligned16(codes) && aligned16(scales) && aligned16(X_hat), CLHA_ERR_INVALID_ARG,
+            "clha_fp4_dequantize: codes, scales and X_hat must be 16-byte aligned");
+    SET_DEVICE(ctx);
+    LaunchScope launch_scope(ctx);
+    CUDA_TRY(launch_fp4_dequantize(ctx->stream, ctx->num_sms, codes, scales, rows, d, fp4_block(format), tensor_scale,
+                                   tensor_scale ? rows / n_scales : 1, X_hat, dtype == CLHA_F32),
+             "clha_fp4_dequantize");
+    return CLHA_OK;
+}
+
+// the checks that the two products share
+static clha_status fp4_product(clha_ctx* ctx, const char* call, clha_fp4_format format, const Fp4Product& a, bool act,
+                               bool y_f32) {
+    const int block = fp4_block(format);
+    REQUIRE(block, CLHA_ERR_INVALID_ARG, "%s: unknown format", call);
+    REQUIRE(a.rows >= 0 && a.K > 0 && a.N > 0 && a.E >= 1 && a.E <= 1024, CLHA_ERR_INVALID_ARG, "%s: bad sizes", call);
+    REQUIRE(a.seg || a.E == 1, CLHA_ERR_INVALID_ARG, "%s: seg == NULL needs E == 1", call);
+    REQUIRE(a.K % 128 == 0 && a.N % 128 == 0, CLHA_ERR_UNSUPPORTED_SHAPE,
+            "%s: input width %d and output width %d must be multiples of 128", call, a.K, a.N);
+    const int64_t lim = (int64_t)1 << 31;
+    REQUIRE(a.rows < lim - 128 && (int64_t)a.E * a.N < lim && a.rows <= (lim * 64) / a.K &&
+                (int64_t)a.E * a.N <= (lim * 64) / a.K,
+            CLHA_ERR_UNSUPPORTED_SHAPE, "%s: operands too large", call);
+    if (a.rows == 0) return CLHA_OK;
+    REQUIRE(a.xq && a.xs && a.wq && a.ws && a.Y && (!act || (a.uq && a.us)), CLHA_ERR_INVALID_ARG, "%s: null pointer", call);
+    REQUIRE(aligned16(a.xq) && aligned16(a.xs) && aligned16(a.wq) && aligned16(a.ws) && aligned16(a.uq) &&
+                aligned16(a.us) && aligned16(a.Y),
+            CLHA_ERR_INVALID_ARG, "%s: codes, scales and the output must be 16-byte aligned", call);
+    SET_DEVICE(ctx);
+    LaunchScope launch_scope(ctx);
+    CUDA_TRY(launch_fp4_matmul(ctx->stream, ctx->num_sms, a, block, y_f32, ctx->d_err), call);
+    return CLHA_OK;
+}
+
+extern "C" clha_status clha_fp4_matmul(clha_ctx* ctx, clha_fp4_format format, const uint8_t* x_codes,
+                                       const uint8_t* x_scales, const float* x_scale, int64_t rows, int d_in,
+                                       const int64_t* seg, int E, const uint8_t* w_codes, const uint8_t* w_scales,
+                                       const float* w_scale, int d_out, void* Y, clha_dtype y_dtype) {
+    CHECK_CTX(ctx);
+    REQUIRE(dtype_size(y_dtype), CLHA_ERR_INVALID_ARG, "clha_fp4_matmul: unknown dtype");
+    const Fp4Product a{x_codes, x_scales, w_codes, w_scales, nullptr, nullptr, x_scale, w_scale, nullptr,
+                       rows, d_in, d_out, seg, E, Y};
+    return fp4_product(ctx, "clha_fp4_matmul", format, a, false, y_dtype == CLHA_F32);
+}
+
+extern "C" clha_status clha_fp4_expert_act(clha_ctx* ctx, clha_fp4_format format, const uint8_t* x_codes,
+                                           const uint8_t* x_scales, const float* x_scale, int64_t rows, int d_model,
+                                           const int64_t* seg, int E, const uint8_t* g_codes, const uint8_t* g_scales,
+                                           const float* g_scale, const uint8_t* u_codes, const uint8_t* u_scales,
+                                           const float* u_scale, int d_ff, void* h) {
+    CHECK_CTX(ctx);
+    const Fp4Product a{x_codes, x_scales, g_codes, g_scales, u_codes, u_scales, x_scale, g_scale, u_scale,
+                       rows, d_model, d_ff, seg, E, h};
+    return fp4_product(ctx, "clha_fp4_expert_act", format, a, true, false);
+}
+
+extern "C" clha_status clha_combine(clha_ctx* ctx, const void* Z, clha_dtype z_dtype, int64_t rows, int d,
+                                    const int32_t* ids, const float* weights, int64_t n, int k, int E,
+                                    const int64_t* seg, const int32_t* perm, const void* add, void* Y,
+                                    clha_dtype y_dtype) {
+    CHECK_CTX(ctx);
+    REQUIRE(dtype_size(z_dtype) && dtype_size(y_dtype), CLHA_ERR_INVALID_ARG, "clha_combine: unknown dtype");
+    REQUIRE(n >= 0 && n < (int64_t)1 << 31 && rows >= 0 && d > 0, CLHA_ERR_INVALID_ARG, "clha_combine: bad sizes");
+    REQUIRE(E >= 1 && E <= 1024 && k >= 1 && k <= E, CLHA_ERR_INVALID_ARG, "clha_combine: need 1 <= k <= E <= 1024");
+    REQUIRE(d % 128 == 0, CLHA_ERR_UNSUPPORTED_SHAPE, "clha_combine: d=%d is not a multiple of 128", d);
+    if (n == 0) return CLHA_OK;
+    REQUIRE(Z && ids && seg && perm && Y, CLHA_ERR_INVALID_ARG, "clha_combine: null pointer");
+    REQUIRE(aligned16(Z) && aligned16(add) && aligned16(Y), CLHA_ERR_INVALID_ARG,
+            "clha_combine: Z, add and Y must be 16-byte aligned");
+    SET_DEVICE(ctx);
+    LaunchScope launch_scope(ctx);
+    CUDA_TRY(launch_combine(ctx->stream, Z, z_dtype == CLHA_F32, rows, d, ids, weights, n, k, E, seg, perm, add, Y,
+                            y_dtype == CLHA_F32, ctx->d_err),
+             "clha_combine");
     return CLHA_OK;
 }

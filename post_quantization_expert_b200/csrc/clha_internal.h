@@ -41,7 +41,8 @@ struct clha_accum {
 
 enum clha_kernel_id {
     KID_ROUTE = 1, KID_GATHER = 2, KID_ACT = 3, KID_COLLECT = 4, KID_AGGREGATE = 5,
-    KID_FACTOR = 6, KID_QUANTIZE = 7, KID_LOSS = 8, KID_DIVERGENCE = 9
+    KID_FACTOR = 6, KID_QUANTIZE = 7, KID_LOSS = 8, KID_DIVERGENCE = 9,
+    KID_GATE = 10, KID_FP4 = 11, KID_FP4_MATMUL = 12, KID_COMBINE = 13
 };
 
 // ------------------------------------------------------------------------------ device helpers
@@ -147,3 +148,28 @@ cudaError_t launch_quantize(cudaStream_t s, int num_sms, const float* U, int n_u
                             int* err, int form);   // form as launch_factor's: the factor U holds
 cudaError_t launch_loss(cudaStream_t s, const void* W, int w_is_f32, const float* W_hat, const float* H,
                         int n_h, int batch, int d_out, int d_in, double* d_loss);
+// ------------------------------------------------------------------ the 4-bit expert layer
+cudaError_t launch_route_gated(cudaStream_t s, int num_sms, const void* logits, int is_f32, int64_t n,
+                               const clha_route_params& rp, const float* bias, int32_t* ids, float* weights,
+                               int32_t* counts, int* err);
+cudaError_t launch_fp4_tensor_scale(cudaStream_t s, int num_sms, const void* X, int x_f32, int batch, int64_t per,
+                                    int block, float* scale, int* err);
+cudaError_t launch_fp4_quantize(cudaStream_t s, int num_sms, const void* X, int x_f32, int64_t n, int d,
+                                const int32_t* perm, int64_t rows, const int64_t* seg, int E, int block, const float* g,
+                                int64_t rows_per_g, uint8_t* codes, uint8_t* scales, int* err);
+cudaError_t launch_fp4_dequantize(cudaStream_t s, int num_sms, const uint8_t* codes, const uint8_t* scales, int64_t rows,
+                                  int d, int block, const float* g, int64_t rows_per_g, void* out, int out_f32);
+// Operands of a product over 4-bit rows: X [rows, K], W (and, for gate and up, U) [E * N, K].
+struct Fp4Product {
+    const uint8_t *xq, *xs, *wq, *ws, *uq, *us;   // codes and tiled scales; uq null: a plain product
+    const float *xg, *wg, *ug;                    // matrix scales: one of X, E of W and of U (null: 1)
+    int64_t rows;
+    int K, N;
+    const int64_t* seg;
+    int E;
+    void* Y;
+};
+cudaError_t launch_fp4_matmul(cudaStream_t s, int num_sms, const Fp4Product& a, int block, int y_f32, int* err);
+cudaError_t launch_combine(cudaStream_t s, const void* Z, int z_f32, int64_t rows, int d, const int32_t* ids,
+                           const float* w, int64_t n, int k, int E, const int64_t* seg, const int32_t* perm,
+                           const void* add, void* Y, int y_f32, int* err);

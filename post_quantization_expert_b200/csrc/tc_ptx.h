@@ -150,6 +150,41 @@ __device__ __forceinline__ void mma_commit(uint32_t bar) {
                  : "memory");
 }
 
+// ------------------------------------------------------------------------------ block-scaled e2m1
+// D[tmem] (+)= A * B over 64 e2m1 values a row, two a byte, with the operands' block scales in TMEM:
+// blocks of 16 with e4m3 scales (scale_vec::4X, one 32-bit cell a row) or blocks of 32 with e8m0 scales
+// (scale_vec::2X, half a cell; the instruction descriptor says which half).
+template <int BLOCK>
+__device__ __forceinline__ void mma_fp4(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc, uint32_t sfa,
+                                        uint32_t sfb, uint32_t accumulate) {
+    static_assert(BLOCK == 16 || BLOCK == 32, "block of 16 or 32");
+    if (BLOCK == 16)
+        asm volatile(
+            "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+            "tcgen05.mma.cta_group::1.kind::mxf4nvf4.block_scale.scale_vec::4X [%0], %1, %2, %3, [%5], [%6], p;\n\t}"
+            ::"r"(d_tmem), "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate), "r"(sfa), "r"(sfb) : "memory");
+    else
+        asm volatile(
+            "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+            "tcgen05.mma.cta_group::1.kind::mxf4.block_scale.scale_vec::2X [%0], %1, %2, %3, [%5], [%6], p;\n\t}"
+            ::"r"(d_tmem), "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate), "r"(sfa), "r"(sfb) : "memory");
+}
+// 32 rows of 16 bytes in shared memory (plain_desc) to 4 TMEM columns, the same 32 lanes in each of the
+// four lane quadrants. Ordered before later tcgen05.mma of the same thread.
+__device__ __forceinline__ void tmem_copy_scales(uint32_t taddr, uint64_t sdesc) {
+    asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(sdesc) : "memory");
+}
+// Shared-memory matrix descriptor of rows of 16 bytes stored one after the other (no swizzle; 8-row
+// groups 128 bytes apart).
+__device__ __forceinline__ uint64_t plain_desc(uint32_t saddr) {
+    return (uint64_t)((saddr >> 4) & 0x3FFF) | ((uint64_t)(128 >> 4) << 32) | ((uint64_t)1 << 46);
+}
+// Instruction descriptor of the block-scaled e2m1 kinds; scale type 0 = e4m3, 1 = e8m0; sf_id: the byte
+// of each 32-bit scale cell that the product starts at (0 or 2).
+__host__ __device__ constexpr uint32_t idesc_fp4(uint32_t e8m0, uint32_t M, uint32_t N, uint32_t sf_id) {
+    return (sf_id << 4) | (1u << 7) | (1u << 10) | ((N >> 3) << 17) | (e8m0 << 23) | ((M >> 7) << 27) | (sf_id << 29);
+}
+
 // 32 lanes x 32 columns of 32-bit: lane i of the warp receives columns [col, col+32) of TMEM lane
 // (lane base of this warp + i).
 __device__ __forceinline__ void tmem_ld_32x32b_x32(uint32_t taddr, uint32_t (&r)[32]) {

@@ -625,3 +625,97 @@ class EPMQCalibration:
         L.clha_quantize(ctx, self.U, 1, self.W_target, 1, self.d_out, self.d, self.bits, q.codes, q.scales, q.zeros,
                         q.W_hat)
         return q
+
+
+class Fp4Layer:
+    """One MoE layer that runs its experts in microscaled 4-bit floating point. The weights are quantized once,
+    at construction (round to nearest; the blocks' scales are all the calibration they need); forward() then is
+      clha_route_gated -> clha_gather (the permutation) -> clha_fp4_quantize (the routed rows)
+      -> clha_fp4_expert_act -> clha_fp4_quantize -> clha_fp4_matmul -> clha_combine.
+    Always-active experts see every token with weight 1: their gate, up and down projections are laid side by
+    side, so that they run as one dense expert whose output is the combination's addend. Buffers are the
+    layer's own; forward() queues work on the context's stream and synchronises nothing, and after one
+    eager call (which sizes the gather's workspace) it can be captured into a graph."""
+
+    def __init__(self, ctx: L.Context, w: MoEWeights, k: int, max_tokens: int, fmt: int = L.FP4_E4M3_16,
+                 score: int = L.SCORE_SOFTMAX, bias: torch.Tensor | None = None, n_groups: int = 1, top_groups: int = 1,
+                 group_rank: int = L.GROUP_MAX, renormalise: bool = True, scale: float = 1.0, timer=NO_TIMER):
+        """w: the layer's weights (bf16 or f32). bias, n_groups, ... scale: as clha_route_gated takes them."""
+        self.ctx, self.k, self.fmt, self.timer, self.max_tokens = ctx, k, fmt, timer, max_tokens
+        self.E, self.d_model, self.d_ff = w.Wd.shape
+        self.gate = dict(score=score, bias=bias, n_groups=n_groups, top_groups=top_groups, group_rank=group_rank,
+                         renormalise=renormalise, scale=scale)
+        dev = self.dev = torch.device("cuda", ctx.device)
+        E, dm, dff = self.E, self.d_model, self.d_ff
+        self.gate_up = [self._weight(m, E, dff, dm) for m in (w.Wg, w.Wu)]
+        self.down = self._weight(w.Wd, E, dm, dff)
+        self.P = L.clha_packed_rows(max_tokens, k, E)
+        self.ids = torch.empty((max_tokens, k), dtype=torch.int32, device=dev)
+        self.weights = torch.empty((max_tokens, k), dtype=torch.float32, device=dev)
+        self.counts = torch.empty(E, dtype=torch.int32, device=dev)
+        self.seg = torch.empty(2 * E + 1, dtype=torch.int64, device=dev)
+        self.perm = torch.empty(self.P, dtype=torch.int32, device=dev)
+        self.x = self._operand(self.P, dm)
+        self.h = torch.empty((self.P, dff), dtype=torch.bfloat16, device=dev)
+        self.hq = self._operand(self.P, dff)
+        self.z = torch.empty((self.P, dm), dtype=torch.float32, device=dev)
+        self.shared = None
+        if w.Sgu is not None:
+            ns, sdff = w.Sgu.shape[0] // 2, w.Sgu.shape[1]
+            side = w.Sd.permute(1, 0, 2).reshape(1, dm, ns * sdff).contiguous()
+            self.shared = ns * sdff
+            self.s_gate_up = [self._weight(m.reshape(1, ns * sdff, dm), 1, ns * sdff, dm) for m in (w.Sg, w.Su)]
+            self.s_down = self._weight(side, 1, dm, ns * sdff)
+            self.sx = self._operand(max_tokens, dm)
+            self.sh = torch.empty((max_tokens, ns * sdff), dtype=torch.bfloat16, device=dev)
+            self.shq = self._operand(max_tokens, ns * sdff)
+
+    def _operand(self, rows: int, d: int):
+        """Code and scale buffers of [rows, d]."""
+        return (torch.empty((rows, d // 2), dtype=torch.uint8, device=self.dev),
+                torch.empty(L.clha_fp4_scale_bytes(self.fmt, rows, d), dtype=torch.uint8, device=self.dev))
+
+    def _weight(self, W, E: int, d_out: int, d_in: int):
+        """(codes, scales, matrix scales) of W [E, d_out, d_in]; the power-of-two format needs no matrix scales."""
+        g = None
+        if self.fmt == L.FP4_E4M3_16:
+            g = torch.empty(E, dtype=torch.float32, device=self.dev)
+            L.clha_fp4_tensor_scale(self.ctx, W, E, d_out, d_in, self.fmt, g)
+        codes, scales = self._operand(E * d_out, d_in)
+        L.clha_fp4_quantize(self.ctx, W, E * d_out, d_in, self.fmt, codes, scales, tensor_scale=g)
+        return codes, scales, g
+
+    def forward(self, X: torch.Tensor, logits: torch.Tensor, Y: torch.Tensor):
+        """Y [n, d_model] (f32 or bf16) of the tokens X [n, d_model] (f32 or bf16) with router logits [n, E];
+        n <= max_tokens. Returns Y."""
+        ctx, t, n, E, k, fmt = self.ctx, self.timer, X.shape[0], self.E, self.k, self.fmt
+        if n > self.max_tokens:
+            raise ValueError(f"{n} tokens in a layer built for {self.max_tokens}")
+        P = L.clha_packed_rows(n, k, E)
+        dm, dff = self.d_model, self.d_ff
+        ids, weights = self.ids[:n], self.weights[:n]
+        with t.span("route"):
+            L.clha_route_gated(ctx, logits, n, E, k, ids, weights, self.counts, **self.gate)
+            L.clha_gather(ctx, X, n, dm, ids, k, E, None, P, self.seg, self.perm)
+        seg = dict(seg=self.seg, E=E)
+        with t.span("quantize"):
+            L.clha_fp4_quantize(ctx, X, n, dm, fmt, *self.x, perm=self.perm, rows=P, **seg)
+        (g, gs, gg), (u, us, gu), (d, ds, gd) = *self.gate_up, self.down
+        with t.span("act"):
+            L.clha_fp4_expert_act(ctx, fmt, *self.x, P, dm, g, gs, u, us, dff, self.h, g_scale=gg, u_scale=gu, **seg)
+        with t.span("quantize"):
+            L.clha_fp4_quantize(ctx, self.h, P, dff, fmt, *self.hq, **seg)
+        with t.span("down"):
+            L.clha_fp4_matmul(ctx, fmt, *self.hq, P, dff, d, ds, dm, self.z, w_scale=gd, **seg)
+        add = None
+        if self.shared:
+            sd, add = self.shared, Y
+            (g, gs, gg), (u, us, gu), (d, ds, gd) = *self.s_gate_up, self.s_down
+            with t.span("shared"):
+                L.clha_fp4_quantize(ctx, X, n, dm, fmt, *self.sx)
+                L.clha_fp4_expert_act(ctx, fmt, *self.sx, n, dm, g, gs, u, us, sd, self.sh, g_scale=gg, u_scale=gu)
+                L.clha_fp4_quantize(ctx, self.sh, n, sd, fmt, *self.shq)
+                L.clha_fp4_matmul(ctx, fmt, *self.shq, n, sd, d, ds, dm, Y, w_scale=gd)
+        with t.span("combine"):
+            L.clha_combine(ctx, self.z, P, dm, ids, weights, n, k, E, self.seg, self.perm, Y, add=add)
+        return Y
