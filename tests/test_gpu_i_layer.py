@@ -194,7 +194,9 @@ def check_product(got, want, mags, K, out):
 @pytest.mark.parametrize("fmt", FMTS)
 @pytest.mark.parametrize("out", [F32, BF16])
 @pytest.mark.parametrize("n,K,N", [(1, 128, 128), (1, 2048, 256), (7, 384, 384), (128, 256, 128), (129, 640, 256),
-                                   (300, 1152, 640), (64, 8192, 128)])
+                                   (300, 1152, 640), (64, 8192, 128),
+                                   # many tiles: pairs of SMs, the last row tile and the last column block halves
+                                   (2600, 640, 2176), (4999, 1152, 1024)])
 def test_matmul(ctx, fmt, out, n, K, N):
     x = torch.randn((n, K), generator=gen(n + K)).to(BF16)
     w = (0.02 * torch.randn((N, K), generator=gen(N))).to(BF16)
@@ -213,7 +215,9 @@ def stacked(w, E):
 @pytest.mark.parametrize("fmt", FMTS)
 @pytest.mark.parametrize("scaled", [False, True])
 @pytest.mark.parametrize("n,E,k,K,N", [(300, 10, 3, 384, 256), (5, 16, 2, 512, 128), (1, 4, 1, 128, 384),
-                                       (1500, 4, 2, 256, 640)])
+                                       (1500, 4, 2, 256, 640),
+                                       # many tiles: pairs of SMs, segments with an odd number of 128-row tiles
+                                       (3001, 10, 3, 384, 640), (2000, 64, 6, 256, 384)])
 def test_expert_products(ctx, fmt, scaled, n, E, k, K, N):
     """Both products over segments: padding rows zero, rows behind the last segment untouched, experts without
     tokens, a scale for each expert."""
@@ -261,7 +265,7 @@ def check_act(h, x64, w64, u64, seg, K):
 
 
 @pytest.mark.parametrize("fmt", FMTS)
-@pytest.mark.parametrize("n,K,N", [(1, 2048, 128), (3, 4096, 256), (130, 128, 384), (257, 640, 128)])
+@pytest.mark.parametrize("n,K,N", [(1, 2048, 128), (3, 4096, 256), (130, 128, 384), (257, 640, 128), (2570, 384, 1024)])
 def test_dense_act(ctx, fmt, n, K, N):
     x = torch.randn((n, K), generator=gen(n)).to(BF16)
     w, u = ((0.05 * torch.randn((N, K), generator=gen(i))).to(BF16) for i in (21, 22))
