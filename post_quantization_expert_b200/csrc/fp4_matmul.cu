@@ -362,6 +362,11 @@ fp4_matmul_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant
 // through shared memory by TMA (boxes of 32 rows x 128 bytes), which cuts off rows behind the end of Y.
 // Tiles of an expert are taken in bands of 8 row tiles, rows fastest, so that the pairs working at one time
 // share about 8 row blocks and as many column blocks of L2.
+//
+// Two warps of their own copy the scales to TMEM, every other scale column each. Such a copy takes about 60
+// cycles in its issuer's order, and a stage of e4m3 scales has twelve: issued by the products' thread they ran
+// in line with its products (measured on 4096 x 16384 -> 9472: 441 us; from one other warp 343, from two 274;
+// without any copy 253). Writing the scales with tcgen05.st from registers took 547.
 template <int BLOCK>
 struct PairCfg {
     static constexpr int APS = 256 / BLOCK / 4;
@@ -372,11 +377,12 @@ struct PairCfg {
     static constexpr int STG_OFF = STAGES * ((STAGE_BYTES + 1023) / 1024 * 1024);
     static constexpr int STAGE_STRIDE = (STAGE_BYTES + 1023) / 1024 * 1024;
     static constexpr int BAR_OFF = STG_OFF + 8 * 4096;
-    static constexpr int SMEM = BAR_OFF + 8 * (2 * STAGES + 3) + 16 + 1024;
+    static constexpr int SMEM = BAR_OFF + 8 * (3 * STAGES + 3) + 16 + 1024;
     static_assert(SMEM <= MAX_SMEM, "shared memory");
     static_assert(256 + STAGES * SF_COLS <= 512, "tensor memory");
 };
 constexpr int kBand = 8;
+constexpr int kPairThreads = 384;   // as above, and warps 10 and 11 for the scales
 
 // The tiles in order: expert after expert, each expert's in bands. A role asks with ascending w.
 struct Walk {
@@ -404,7 +410,7 @@ struct Walk {
 };
 
 template <int BLOCK, bool ACT, typename OUT>
-__global__ void __launch_bounds__(kThreads, 1)
+__global__ void __launch_bounds__(kPairThreads, 1)
 fp4_matmul_pair_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ CUtensorMap tmXs,
                        const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUtensorMap tmWs,
                        const __grid_constant__ CUtensorMap tmU, const __grid_constant__ CUtensorMap tmUs,
@@ -419,7 +425,8 @@ fp4_matmul_pair_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_con
     const uint32_t tfull = empty0 + 8 * C::STAGES;        // each CTA: the accumulator holds a finished tile
     const uint32_t tempty = tfull + 8;                    // leader: both CTAs' epilogues have read it
     const uint32_t drain = tempty + 8;
-    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 2 * C::STAGES + 3);
+    const uint32_t sready0 = drain + 8;                   // leader: a stage's scales are on their way to TMEM
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 3 * C::STAGES + 3);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
     const uint32_t rank = tc::cluster_ctarank();
     const bool leader = rank == 0;
@@ -429,10 +436,11 @@ fp4_matmul_pair_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_con
         for (int s = 0; s < C::STAGES; ++s) {
             tc::mbar_init(full0 + 8 * s, 1);
             tc::mbar_init(empty0 + 8 * s, 1);
+            tc::mbar_init(sready0 + 8 * s, 2);            // one arrival per scale warp
         }
         tc::mbar_init(tfull, 1);
         tc::mbar_init(tempty, 16);                        // one arrival per epilogue warp of either CTA
-        tc::mbar_init(drain, 1);
+        tc::mbar_init(drain, 3);                          // the products' thread and the scale warps
         *abort_flag = 0;
         tc::fence_barrier_init();
     }
@@ -496,17 +504,13 @@ fp4_matmul_pair_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_con
                 tc::fence_after_sync();
                 for (int kb = 0; kb < nk; ++kb, ++it) {
                     const int s = it % C::STAGES;
-                    if (!tc::mbar_wait_bounded(full0 + 8 * s, (it / C::STAGES) & 1, abort_flag)) { ok = false; break; }
+                    const uint32_t ph = (it / C::STAGES) & 1;
+                    if (!tc::mbar_wait_bounded(full0 + 8 * s, ph, abort_flag) ||
+                        !tc::mbar_wait_bounded(sready0 + 8 * s, ph, abort_flag)) { ok = false; break; }
                     tc::fence_after_sync();
                     const uint32_t a = tc::smem_u32(smem + s * C::STAGE_STRIDE);
-                    const uint32_t b = a + TILE_BYTES, sf = a + 2 * TILE_BYTES;
+                    const uint32_t b = a + TILE_BYTES;
                     const uint32_t ta = tmem + 256 + s * C::SF_COLS, tb = ta + C::APS * 4;
-#pragma unroll
-                    for (int j = 0; j < C::APS; ++j) {
-                        tc::tmem_copy_scales_pair(ta + 4 * j, tc::plain_desc(sf + j * 512));
-                        tc::tmem_copy_scales_pair(tb + 8 * j, tc::plain_desc(sf + C::SF_BYTES + j * 512));
-                        tc::tmem_copy_scales_pair(tb + 8 * j + 4, tc::plain_desc(sf + 2 * C::SF_BYTES + j * 512));
-                    }
                     const int steps = p.K - kb * 256 >= 256 ? 4 : 2;   // K is a multiple of 128
 #pragma unroll
                     for (int kk = 0; kk < 4; ++kk) {
@@ -520,6 +524,31 @@ fp4_matmul_pair_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_con
                 }
                 if (ok) tc::mma_commit_pair(tfull, 0x3);
             }
+        }
+        __syncwarp();
+    } else if (warp >= 10) {
+        if (lane == 0 && leader) {
+            Walk k;
+            int it = 0;
+            bool ok = true;
+            for (int64_t w = pair; ok && k.at(p, w); w += npairs)
+                for (int kb = 0; kb < nk; ++kb, ++it) {
+                    const int s = it % C::STAGES;
+                    if (!tc::mbar_wait_bounded(full0 + 8 * s, (it / C::STAGES) & 1, abort_flag)) { ok = false; break; }
+                    tc::fence_after_sync();
+                    const uint32_t sf = tc::smem_u32(smem + s * C::STAGE_STRIDE) + 2 * TILE_BYTES;
+                    const uint32_t ta = tmem + 256 + s * C::SF_COLS, tb = ta + C::APS * 4;
+#pragma unroll
+                    for (int j = 0; j < C::APS; ++j) {
+                        if ((j & 1) != warp - 10) continue;
+                        tc::tmem_copy_scales_pair(ta + 4 * j, tc::plain_desc(sf + j * 512));
+                        tc::tmem_copy_scales_pair(tb + 8 * j, tc::plain_desc(sf + C::SF_BYTES + j * 512));
+                        tc::tmem_copy_scales_pair(tb + 8 * j + 4, tc::plain_desc(sf + 2 * C::SF_BYTES + j * 512));
+                    }
+                    tc::mma_commit_pair(sready0 + 8 * s, 0x1);
+                }
+            // the copies that this thread issued are done before the CTA gives its TMEM back
+            tc::mma_commit_pair(drain, 0x1);
         }
         __syncwarp();
     } else {
@@ -649,7 +678,7 @@ cudaError_t launch_pair(cudaStream_t s, int num_sms, const Fp4Product& a, int* e
     const int tile_n = ACT ? 128 : 256;
     MatmulArgs p{a.rows, a.K, a.N, a.seg, a.E, a.xg, a.wg, a.ug, a.Y, (a.N + tile_n - 1) / tile_n, 1, err};
     cudaLaunchConfig_t cfg = {};
-    cfg.blockDim = dim3(kThreads);
+    cfg.blockDim = dim3(kPairThreads);
     cfg.dynamicSmemBytes = C::SMEM;
     cfg.stream = s;
     cfg.gridDim = dim3((unsigned)(num_sms / 2 * 2));
