@@ -9,6 +9,7 @@ fallback.
 from __future__ import annotations
 
 import ctypes as C
+import functools
 import os
 import sys
 
@@ -419,18 +420,37 @@ def clha_unpack_upper(ctx: Context, packed, n_outer: int, outer_stride: int, n_i
                                         _mat_ptr(S, first, n_outer, outer_stride, n_inner, d)))
 
 
-def _check_sizes(call: str, **want):
-    """Refuses a tensor with fewer elements than the call would read or write: name=(tensor, elements)."""
-    for name, (t, numel) in want.items():
-        if t is not None and t.numel() < numel:
-            raise ValueError(f"{call}: {name} has {t.numel()} elements, needs {numel}")
+def _arg(call: str, dev: int, name: str, t, numel: int, dtype):
+    """Pointer of a tensor argument, or NULL for None, after refusing another element type, fewer elements than
+    the call reads or writes, gaps, or another device (one function, because these calls take microseconds)."""
+    if t is None:
+        return None
+    if t.dtype is not dtype:
+        raise TypeError(f"{call}: {name} is {t.dtype}, needs {dtype}")
+    if t.numel() < numel:
+        raise ValueError(f"{call}: {name} has {t.numel()} elements, needs {numel}")
+    if not t.is_contiguous():
+        raise ValueError(f"{call}: {name} is not contiguous; libclha takes dense row-major arrays")
+    if t.get_device() != dev:
+        raise ValueError(f"{call}: {name} is on {t.device}, the context on device {dev}")
+    return t.data_ptr()
 
 
-def _check_types(call: str, **want):
-    """Refuses a tensor of another element type: name=(tensor, dtype)."""
-    for name, (t, dtype) in want.items():
-        if t is not None and t.dtype != dtype:
-            raise TypeError(f"{call}: {name} is {t.dtype}, needs {dtype}")
+def _device(ctx) -> int:
+    """The context's device; -1 (the host's number in get_device) without one, so that sizes can be checked."""
+    return -1 if ctx is None else ctx.device
+
+
+def _float_arg(call: str, dev: int, name: str, t, numel: int):
+    """_arg for a float32 or bfloat16 tensor that may not be None: (pointer, clha_dtype)."""
+    if t.dtype is torch.bfloat16:
+        return _arg(call, dev, name, t, numel, torch.bfloat16), BF16
+    return _arg(call, dev, name, t, numel, torch.float32), F32
+
+
+@functools.lru_cache(maxsize=256)
+def _route_params(*fields):
+    return RouteParams(*fields)
 
 
 def clha_route_gated(ctx: Context, logits, n: int, E: int, k: int, ids, weights, counts, score: int = SCORE_SOFTMAX,
@@ -438,13 +458,12 @@ def clha_route_gated(ctx: Context, logits, n: int, E: int, k: int, ids, weights,
                      renormalise: bool = True, scale: float = 1.0):
     """Top-k routing with gate weights: ids int32 [n, k], weights float32 [n, k], counts int32 [E]; logits
     [n, E] float32 or bfloat16, bias float32 [E] or None (added for the choice only)."""
-    _check_sizes("clha_route_gated", logits=(logits, n * E), ids=(ids, n * k), weights=(weights, n * k),
-                 counts=(counts, E), bias=(bias, E))
-    _check_types("clha_route_gated", ids=(ids, torch.int32), weights=(weights, torch.float32),
-                 counts=(counts, torch.int32), bias=(bias, torch.float32))
-    rp = RouteParams(E, k, score, n_groups, top_groups, group_rank, int(renormalise), scale)
-    ctx._check(load().clha_route_gated(ctx.handle, _p(logits), _dtype(logits), n, C.byref(rp), _p(bias), _p(ids),
-                                       _p(weights), _p(counts)))
+    call, dev = "clha_route_gated", _device(ctx)
+    lp, lt = _float_arg(call, dev, "logits", logits, n * E)
+    bp, ip = _arg(call, dev, "bias", bias, E, torch.float32), _arg(call, dev, "ids", ids, n * k, torch.int32)
+    wp, cp = _arg(call, dev, "weights", weights, n * k, torch.float32), _arg(call, dev, "counts", counts, E, torch.int32)
+    rp = _route_params(E, k, score, n_groups, top_groups, group_rank, renormalise, scale)
+    ctx._check(load().clha_route_gated(ctx.handle, lp, lt, n, C.byref(rp), bp, ip, wp, cp))
 
 
 def clha_fp4_scale_bytes(fmt: int, rows: int, d: int) -> int:
@@ -454,16 +473,17 @@ def clha_fp4_scale_bytes(fmt: int, rows: int, d: int) -> int:
 
 def clha_fp4_tensor_scale(ctx: Context, X, batch: int, rows: int, d: int, fmt: int, scale):
     """scale (float32 [batch]) of the matrices X [batch, rows, d]: max|x| over the format's largest number."""
-    _check_sizes("clha_fp4_tensor_scale", X=(X, batch * rows * d), scale=(scale, batch))
-    _check_types("clha_fp4_tensor_scale", scale=(scale, torch.float32))
-    ctx._check(load().clha_fp4_tensor_scale(ctx.handle, _p(X), _dtype(X), batch, rows, d, fmt, _p(scale)))
+    call, dev = "clha_fp4_tensor_scale", _device(ctx)
+    xp, xt = _float_arg(call, dev, "X", X, batch * rows * d)
+    sp = _arg(call, dev, "scale", scale, batch, torch.float32)
+    ctx._check(load().clha_fp4_tensor_scale(ctx.handle, xp, xt, batch, rows, d, fmt, sp))
 
 
-def _fp4_sizes(call: str, fmt: int, rows: int, d: int, codes, scales, tensor_scale=None):
-    """Checks of one operand's buffers: codes [rows, d / 2], the tiled scales, float32 matrix scales."""
-    _check_types(call, codes=(codes, torch.uint8), scales=(scales, torch.uint8),
-                 tensor_scale=(tensor_scale, torch.float32))
-    _check_sizes(call, codes=(codes, rows * d // 2), scales=(scales, load().clha_fp4_scale_bytes(fmt, rows, d)))
+def _operand_args(call: str, dev: int, name: str, fmt: int, rows: int, d: int, codes, scales):
+    """Pointers of one operand's codes [rows, d / 2] and tiled scales."""
+    return (_arg(call, dev, name + "codes", codes, rows * d // 2, torch.uint8),
+            _arg(call, dev, name + "scales", scales, (rows + 127) // 128 * 128 * (d // (16 if fmt == FP4_E4M3_16 else 32)),
+                 torch.uint8))
 
 
 def clha_fp4_quantize(ctx: Context, X, n: int, d: int, fmt: int, codes, scales, tensor_scale=None, perm=None,
@@ -471,56 +491,59 @@ def clha_fp4_quantize(ctx: Context, X, n: int, d: int, fmt: int, codes, scales, 
     """codes uint8 [rows, d / 2] and tiled scales (clha_fp4_scale_bytes) of X [n, d], or, with perm (int32 [rows]),
     of the rows X[perm[r]] (zeros where negative), below seg[E] only if seg is given. tensor_scale: float32,
     each entry for an equal share of the rows."""
+    call, dev = "clha_fp4_quantize", _device(ctx)
     rows = n if rows is None else rows
-    _fp4_sizes("clha_fp4_quantize", fmt, rows, d, codes, scales, tensor_scale)
-    _check_sizes("clha_fp4_quantize", X=(X, n * d), perm=(perm, rows), seg=(seg, 2 * E + 1))
-    _check_types("clha_fp4_quantize", perm=(perm, torch.int32), seg=(seg, torch.int64))
-    ctx._check(load().clha_fp4_quantize(ctx.handle, _p(X), _dtype(X), n, d, _p(perm), rows, _p(seg), E, fmt,
-                                        _p(tensor_scale), 0 if tensor_scale is None else tensor_scale.numel(), _p(codes),
-                                        _p(scales)))
+    xp, xt = _float_arg(call, dev, "X", X, n * d)
+    cp, sp = _operand_args(call, dev, "", fmt, rows, d, codes, scales)
+    pp, gp = _arg(call, dev, "perm", perm, rows, torch.int32), _arg(call, dev, "seg", seg, 2 * E + 1, torch.int64)
+    tp = _arg(call, dev, "tensor_scale", tensor_scale, 1, torch.float32)
+    nt = 0 if tensor_scale is None else tensor_scale.numel()
+    ctx._check(load().clha_fp4_quantize(ctx.handle, xp, xt, n, d, pp, rows, gp, E, fmt, tp, nt, cp, sp))
 
 
 def clha_fp4_dequantize(ctx: Context, codes, scales, rows: int, d: int, fmt: int, X_hat, tensor_scale=None):
     """X_hat [rows, d] (float32 or bfloat16) = the values that codes and scales stand for."""
-    _fp4_sizes("clha_fp4_dequantize", fmt, rows, d, codes, scales, tensor_scale)
-    _check_sizes("clha_fp4_dequantize", X_hat=(X_hat, rows * d))
-    ctx._check(load().clha_fp4_dequantize(ctx.handle, _p(codes), _p(scales), rows, d, fmt, _p(tensor_scale),
-                                          0 if tensor_scale is None else tensor_scale.numel(), _p(X_hat),
-                                          _dtype(X_hat)))
+    call, dev = "clha_fp4_dequantize", _device(ctx)
+    cp, sp = _operand_args(call, dev, "", fmt, rows, d, codes, scales)
+    xp, xt = _float_arg(call, dev, "X_hat", X_hat, rows * d)
+    tp = _arg(call, dev, "tensor_scale", tensor_scale, 1, torch.float32)
+    nt = 0 if tensor_scale is None else tensor_scale.numel()
+    ctx._check(load().clha_fp4_dequantize(ctx.handle, cp, sp, rows, d, fmt, tp, nt, xp, xt))
 
 
 def clha_fp4_matmul(ctx: Context, fmt: int, x_codes, x_scales, rows: int, d_in: int, w_codes, w_scales, d_out: int, Y,
                     x_scale=None, w_scale=None, seg=None, E: int = 1):
     """Y [rows, d_out] (float32 or bfloat16) = X W^T of 4-bit operands; with seg, expert e's segment meets W[e]
     of w_codes [E, d_out, d_in / 2]. x_scale float32 [1], w_scale float32 [E]."""
-    _fp4_sizes("clha_fp4_matmul", fmt, rows, d_in, x_codes, x_scales, x_scale)
-    _fp4_sizes("clha_fp4_matmul", fmt, E * d_out, d_in, w_codes, w_scales, w_scale)
-    _check_sizes("clha_fp4_matmul", Y=(Y, rows * d_out), seg=(seg, 2 * E + 1), x_scale=(x_scale, 1), w_scale=(w_scale, E))
-    _check_types("clha_fp4_matmul", seg=(seg, torch.int64))
-    ctx._check(load().clha_fp4_matmul(ctx.handle, fmt, _p(x_codes), _p(x_scales), _p(x_scale), rows, d_in, _p(seg), E,
-                                      _p(w_codes), _p(w_scales), _p(w_scale), d_out, _p(Y), _dtype(Y)))
+    call, dev = "clha_fp4_matmul", _device(ctx)
+    xc, xs = _operand_args(call, dev, "x_", fmt, rows, d_in, x_codes, x_scales)
+    wc, ws = _operand_args(call, dev, "w_", fmt, E * d_out, d_in, w_codes, w_scales)
+    yp, yt = _float_arg(call, dev, "Y", Y, rows * d_out)
+    xg, wg = _arg(call, dev, "x_scale", x_scale, 1, torch.float32), _arg(call, dev, "w_scale", w_scale, E, torch.float32)
+    sp = _arg(call, dev, "seg", seg, 2 * E + 1, torch.int64)
+    ctx._check(load().clha_fp4_matmul(ctx.handle, fmt, xc, xs, xg, rows, d_in, sp, E, wc, ws, wg, d_out, yp, yt))
 
 
 def clha_fp4_expert_act(ctx: Context, fmt: int, x_codes, x_scales, rows: int, d_model: int, g_codes, g_scales, u_codes,
                         u_scales, d_ff: int, h, x_scale=None, g_scale=None, u_scale=None, seg=None, E: int = 1):
     """h [rows, d_ff] bfloat16 = SiLU(X Wg^T) * (X Wu^T) of 4-bit operands; arguments as clha_fp4_matmul's."""
-    call = "clha_fp4_expert_act"
-    _fp4_sizes(call, fmt, rows, d_model, x_codes, x_scales, x_scale)
-    _fp4_sizes(call, fmt, E * d_ff, d_model, g_codes, g_scales, g_scale)
-    _fp4_sizes(call, fmt, E * d_ff, d_model, u_codes, u_scales, u_scale)
-    _check_sizes(call, h=(h, rows * d_ff), seg=(seg, 2 * E + 1), x_scale=(x_scale, 1), g_scale=(g_scale, E),
-                 u_scale=(u_scale, E))
-    _check_types(call, seg=(seg, torch.int64), h=(h, torch.bfloat16))
-    ctx._check(load().clha_fp4_expert_act(ctx.handle, fmt, _p(x_codes), _p(x_scales), _p(x_scale), rows, d_model,
-                                          _p(seg), E, _p(g_codes), _p(g_scales), _p(g_scale), _p(u_codes), _p(u_scales),
-                                          _p(u_scale), d_ff, _p(h)))
+    call, dev = "clha_fp4_expert_act", _device(ctx)
+    xc, xs = _operand_args(call, dev, "x_", fmt, rows, d_model, x_codes, x_scales)
+    gc, gs = _operand_args(call, dev, "g_", fmt, E * d_ff, d_model, g_codes, g_scales)
+    uc, us = _operand_args(call, dev, "u_", fmt, E * d_ff, d_model, u_codes, u_scales)
+    xg, gg = _arg(call, dev, "x_scale", x_scale, 1, torch.float32), _arg(call, dev, "g_scale", g_scale, E, torch.float32)
+    ug, sp = _arg(call, dev, "u_scale", u_scale, E, torch.float32), _arg(call, dev, "seg", seg, 2 * E + 1, torch.int64)
+    hp = _arg(call, dev, "h", h, rows * d_ff, torch.bfloat16)
+    ctx._check(load().clha_fp4_expert_act(ctx.handle, fmt, xc, xs, xg, rows, d_model, sp, E, gc, gs, gg, uc, us, ug, d_ff,
+                                          hp))
 
 
 def clha_combine(ctx: Context, Z, rows: int, d: int, ids, weights, n: int, k: int, E: int, seg, perm, Y, add=None):
     """Y [n, d] = add + sum_j weights[:, j] * (the row of Z that holds the token in expert ids[:, j]'s segment)."""
-    _check_sizes("clha_combine", Z=(Z, rows * d), ids=(ids, n * k), weights=(weights, n * k), seg=(seg, 2 * E + 1),
-                 perm=(perm, rows), Y=(Y, n * d), add=(add, n * d))
-    _check_types("clha_combine", ids=(ids, torch.int32), weights=(weights, torch.float32), seg=(seg, torch.int64),
-                 perm=(perm, torch.int32), add=(add, Y.dtype))
-    ctx._check(load().clha_combine(ctx.handle, _p(Z), _dtype(Z), rows, d, _p(ids), _p(weights), n, k, E, _p(seg),
-                                   _p(perm), _p(add), _p(Y), _dtype(Y)))
+    call, dev = "clha_combine", _device(ctx)
+    zp, zt = _float_arg(call, dev, "Z", Z, rows * d)
+    yp, yt = _float_arg(call, dev, "Y", Y, n * d)
+    ip, wp = _arg(call, dev, "ids", ids, n * k, torch.int32), _arg(call, dev, "weights", weights, n * k, torch.float32)
+    sp, pp = _arg(call, dev, "seg", seg, 2 * E + 1, torch.int64), _arg(call, dev, "perm", perm, rows, torch.int32)
+    ap = _arg(call, dev, "add", add, n * d, Y.dtype)
+    ctx._check(load().clha_combine(ctx.handle, zp, zt, rows, d, ip, wp, n, k, E, sp, pp, ap, yp, yt))

@@ -6,12 +6,20 @@
 // to the lower expert (and the lower group). The weights are the scores s (without the bias) of the
 // chosen experts, divided by their sum where asked, times a constant.
 //
-// One warp a token, the values in registers (lane i holds experts i, i + 32, ...): HBM-bound for many
-// tokens (4 E bytes a token), latency-bound for few. The order of the choices is that of exact
-// arithmetic to float64's precision, although they are float32 here: two choices nearer than the float32
-// error bound (see `slack`) make the token repeat the selection in float64, so that a rounding never picks
-// the expert. Without a bias, unless groups are ranked by sums, the logits themselves are compared
-// (both scores increase with them), which is exact at once.
+// HBM-bound in principle (E logits in, 8 k bytes out), issue-bound in fact: k rounds of an arg-max. So a
+// token takes only as many lanes as give each 8 experts or more (4 lanes for 32 experts, 8 for 64, ... all 32
+// from 256 on; the lanes of a token hold consecutive experts), and a round is a float maximum over the
+// lane, log2(lanes) exchanges, a vote for the first lane that has it, and a scan of the winner's 8 values.
+// Groups fit this where a group is a power of two of whole lanes; other group sizes, more than 512 experts, and
+// k above twice the lanes take the general kernel (a warp a token, lane i holds experts i, i + 32, ...).
+// 32768 tokens x 64 experts, top 6: general 44 us, this one ROUTE_E64; 9973 x 256 in 8 groups, top 8: general 87 us,
+// this one ROUTE_WIDE.
+//
+// The order of the choices is that of exact arithmetic to float64's precision, although they are float32
+// here: two choices nearer than the float32 error bound (see `choice_slack`) make a warp repeat the token's
+// selection in float64, so that a rounding never picks the expert. Without a bias, unless groups are
+// ranked by sums, the logits themselves are compared (both scores increase with them), which is exact at
+// once.
 #include "clha_internal.h"
 
 namespace {
@@ -69,6 +77,17 @@ __device__ __forceinline__ void warp_best(F& v, int& i) {
     }
 }
 
+// Bound on the difference of two float32 choices whose exact order it leaves open. A sigmoid, 1 / (1 + e), is off by
+// less than 2^-24 through e (2^-22 of it, times s (1 - s) <= 1/4) and 2^-23 of itself through the sum and the
+// division: 2^-22. A softmax is off by less than 2^-18 of the largest score: 2^-22 and the rounded argument's
+// 0.37 2^-24 through the exponential, as much through the sum, whose up to 37 roundings add 37 2^-24, and 2^-22
+// through the division and the product. A biased choice adds 2^-24 of its size. Twice that for the two.
+// (Sums of two are off by twice as much and a rounding of their own: three times the bound.)
+template <typename F>
+__device__ __forceinline__ F choice_slack(bool sigmoid, F top_score, F largest_choice) {
+    return (sigmoid ? (F)0x1p-21f : (F)0x1p-17f * top_score) + (F)0x1p-23f * largest_choice;
+}
+
 // One token's selection in the arithmetic of F. Lane j < k (and j + 32, ...) writes the j-th expert and its
 // weight. Returns false, with nothing written, where a decision was nearer than the error bound.
 template <typename F, int VPL>
@@ -115,11 +134,8 @@ __device__ __forceinline__ bool select_token(const GateArgs& p, const float (&l)
             }
         }
     }
-    // Bound on the difference of two float32 choices whose exact order it leaves open: a score is off by
-    // less than 2^-18 of the largest (exponential, a sum of up to 1024 terms, a division), a biased one by
-    // another 2^-24 of its size; doubled, and doubled again for sums of two.
     F slack = 0;
-    if (!kExact && !by_logit) slack = (F)0x1p-16f * top_score + (F)0x1p-21f * warp_max(big);
+    if (!kExact && !by_logit) slack = choice_slack(p.sigmoid != 0, top_score, warp_max(big));
 
     if (p.n_groups > 1) {
         // rank every group (all lanes hold it), then keep the first top_groups
@@ -163,7 +179,7 @@ __device__ __forceinline__ bool select_token(const GateArgs& p, const float (&l)
                 if ((open >> i & 1) && (bi == 0x7fffffff || rank[i] > bv)) { bv = rank[i]; bi = lane + 32 * i; }
             warp_best(bv, bi);
             if (r == p.top_groups) {
-                if (!kExact && !by_logit && last - bv <= 2 * slack) return false;
+                if (!kExact && !by_logit && last - bv <= 3 * slack) return false;
                 break;
             }
             last = bv;
@@ -247,26 +263,254 @@ __global__ void __launch_bounds__(kWarps * 32) route_gated_kernel(GateArgs p, in
     }
 }
 
+// ------------------------------------------------------------------ LPT lanes a token, VPL experts a lane
+template <int LPT, typename F>
+__device__ __forceinline__ F lanes_max(F v) {
+#pragma unroll
+    for (int o = LPT / 2; o; o >>= 1) v = fmaxf(v, __shfl_xor_sync(kAll, v, o));
+    return v;
+}
+template <int LPT>
+__device__ __forceinline__ float lanes_sum(float v) {
+#pragma unroll
+    for (int o = LPT / 2; o; o >>= 1) v += __shfl_xor_sync(kAll, v, o);
+    return v;
+}
+
+template <typename T, int VPL>
+__device__ __forceinline__ void load_run(const T* p, float (&l)[VPL]) {   // 16-byte aligned, VPL a multiple of 8
+#pragma unroll
+    for (int i = 0; i < VPL; i += 8) {
+        if (sizeof(T) == 4) {
+            const float4 a = __ldg(reinterpret_cast<const float4*>(p + i));
+            const float4 b = __ldg(reinterpret_cast<const float4*>(p + i) + 1);
+            l[i] = a.x; l[i + 1] = a.y; l[i + 2] = a.z; l[i + 3] = a.w;
+            l[i + 4] = b.x; l[i + 5] = b.y; l[i + 6] = b.z; l[i + 7] = b.w;
+        } else {
+            const uint4 a = __ldg(reinterpret_cast<const uint4*>(p + i));
+            const uint32_t w[4] = {a.x, a.y, a.z, a.w};
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                l[i + 2 * j] = __uint_as_float(w[j] << 16);
+                l[i + 2 * j + 1] = __uint_as_float(w[j] & 0xffff0000u);
+            }
+        }
+    }
+}
+
+// Where a token needs float64: the whole warp takes it, as the general kernel would.
+template <typename T, int WPL>
+__device__ __noinline__ void exact_token(const GateArgs& p, int64_t t, int lane, int* hist) {
+    float l[WPL];
+#pragma unroll
+    for (int i = 0; i < WPL; ++i) {
+        const int e = lane + 32 * i;
+        l[i] = e < p.E ? load_logit<T>(p.logits, t * p.E + e) : 0.f;
+        if (!isfinite(l[i])) l[i] = 0.f;
+    }
+    select_token<double, WPL>(p, l, t, lane, hist);
+}
+
+template <typename T, int LPT, int VPL>
+__global__ void __launch_bounds__(kWarps * 32) route_lanes_kernel(GateArgs p, int one_block, int vec) {
+    constexpr int TPW = 32 / LPT;                            // tokens a warp
+    extern __shared__ int hist[];
+    for (int e = threadIdx.x; e < p.E; e += blockDim.x) hist[e] = 0;
+    __syncthreads();
+    const int lane = threadIdx.x & 31, sub = lane & (LPT - 1), first = lane & ~(LPT - 1);
+    const unsigned mine = LPT == 32 ? kAll : ((1u << LPT) - 1) << first;     // the token's lanes
+    const int e0 = sub * VPL;
+    const bool by_logit = !p.bias && (p.n_groups == 1 || !p.top2);
+    const int64_t per_block = kWarps * TPW;
+    float bias[VPL];
+    if (p.bias) {
+#pragma unroll
+        for (int i = 0; i < VPL; ++i) {
+            bias[i] = e0 + i < p.E ? __ldg(p.bias + e0 + i) : 0.f;
+            if (!isfinite(bias[i])) {                        // recorded; taken as 0
+                clha_record_error(p.err, CLHA_ERR_NONFINITE, 0, e0 + i, KID_GATE);
+                bias[i] = 0.f;
+            }
+        }
+    }
+    for (int64_t tb = (int64_t)blockIdx.x * per_block + (threadIdx.x >> 5) * TPW; tb < p.n;
+         tb += (int64_t)gridDim.x * per_block) {
+        const int64_t t = tb + lane / LPT;
+        const bool real = t < p.n;
+        float c[VPL], s[VPL];
+        const T* row = reinterpret_cast<const T*>(p.logits) + (real ? t : 0) * p.E;
+        if (vec && e0 + VPL <= p.E) {
+            load_run<T, VPL>(row + e0, c);
+        } else {
+#pragma unroll
+            for (int i = 0; i < VPL; ++i) c[i] = e0 + i < p.E ? load_logit<T>(row, e0 + i) : -INFINITY;
+        }
+        bool bad = false;
+#pragma unroll
+        for (int i = 0; i < VPL; ++i)
+            if (e0 + i < p.E && !isfinite(c[i])) { bad = true; c[i] = 0.f; }   // recorded; the ids stay in range
+        if (bad && real) clha_record_error(p.err, CLHA_ERR_NONFINITE, (int)(t & 0x7fffffff), 0, KID_GATE);
+
+        float top_score = 1.f;
+        if (!p.sigmoid) {
+            float m = c[0], sum = 0.f;
+#pragma unroll
+            for (int i = 1; i < VPL; ++i) m = fmaxf(m, c[i]);
+            m = lanes_max<LPT>(m);
+#pragma unroll
+            for (int i = 0; i < VPL; ++i) {
+                s[i] = expf(c[i] - m);                       // past E: exp(-inf) = 0
+                sum += s[i];
+            }
+            top_score = 1.f / lanes_sum<LPT>(sum);
+#pragma unroll
+            for (int i = 0; i < VPL; ++i) s[i] *= top_score;
+        } else {
+#pragma unroll
+            for (int i = 0; i < VPL; ++i) s[i] = 1.f / (1.f + expf(-c[i]));
+        }
+        float slack = 0.f;
+        if (!by_logit) {
+            float big = 0.f;
+#pragma unroll
+            for (int i = 0; i < VPL; ++i) {
+                c[i] = e0 + i < p.E ? (p.bias ? s[i] + bias[i] : s[i]) : -INFINITY;
+                if (e0 + i < p.E) big = fmaxf(big, fabsf(c[i]));
+            }
+            slack = choice_slack(p.sigmoid != 0, top_score, lanes_max<LPT>(big));
+        }
+        bool open = false;                                   // a decision inside the error bound
+        if (p.n_groups > 1) {
+            const int q = p.E / p.n_groups / VPL;            // lanes a group, a power of two
+            float a = -INFINITY, b = -INFINITY;              // the two largest choices of the group
+#pragma unroll
+            for (int i = 0; i < VPL; ++i) {
+                b = fmaxf(b, fminf(a, c[i]));
+                a = fmaxf(a, c[i]);
+            }
+            for (int o = 1; o < q; o <<= 1) {
+                const float oa = __shfl_xor_sync(kAll, a, o), ob = __shfl_xor_sync(kAll, b, o);
+                b = fmaxf(fmaxf(b, ob), fminf(a, oa));
+                a = fmaxf(a, oa);
+            }
+            const bool in = e0 < p.E;
+            const float rank = !in ? -INFINITY : p.top2 ? a + b : a;
+            const int g = sub / q;
+            int ahead = 0;
+            float above = INFINITY, below = -INFINITY;       // the last kept and the first dropped rank
+            for (int h = 0; h < p.n_groups; ++h) {
+                const float r = __shfl_sync(kAll, rank, first + h * q);
+                ahead += r > rank || (r == rank && h < g);
+            }
+            const bool kept = in && ahead < p.top_groups;
+            if (!by_logit && p.top_groups < p.n_groups) {
+                if (in && kept) above = rank;
+                if (in && !kept) below = rank;
+                above = -lanes_max<LPT>(-above);
+                below = lanes_max<LPT>(below);
+                open = above - below <= 3 * slack;
+            }
+            if (!kept) {
+#pragma unroll
+                for (int i = 0; i < VPL; ++i) c[i] = -INFINITY;
+            }
+        }
+        float sum = 0.f, last = INFINITY, s0 = 0.f, s1 = 0.f;
+        int i0 = 0, i1 = 0;
+        const int rounds = by_logit ? p.k : p.k + 1;         // one more, to see how near the first loser is
+        for (int r = 0; r < rounds; ++r) {
+            float m = c[0];
+#pragma unroll
+            for (int i = 1; i < VPL; ++i) m = fmaxf(m, c[i]);
+            const float best = lanes_max<LPT>(m);
+            if (!by_logit && r > 0 && last - best <= slack) open = true;
+            if (r == p.k) break;
+            last = best;
+            const unsigned who = __ballot_sync(kAll, m == best) & mine;
+            const int owner = __ffs(who) - 1;
+            int idx = 0;
+            float sv = 0.f;
+#pragma unroll
+            for (int i = VPL - 1; i >= 0; --i)               // the first of the lane's values that is the largest
+                if (c[i] == m) { idx = i; sv = s[i]; }
+            if (owner == lane) {
+#pragma unroll
+                for (int i = 0; i < VPL; ++i)
+                    if (i == idx) c[i] = -INFINITY;
+            }
+            const int e = __shfl_sync(kAll, e0 + idx, owner);
+            sv = __shfl_sync(kAll, sv, owner);
+            sum += sv;
+            if (r == sub) { i0 = e; s0 = sv; }
+            if (r == sub + LPT) { i1 = e; s1 = sv; }
+        }
+        if (p.renorm && !(sum > 1e-30f)) open = true;        // float32 scores that underflow
+        if (real && !open) {
+            const float f = p.renorm ? p.scale / sum : p.scale;
+            if (sub < p.k) {
+                p.ids[t * p.k + sub] = i0;
+                p.weights[t * p.k + sub] = s0 * f;
+                atomicAdd(&hist[i0], 1);
+            }
+            if (sub + LPT < p.k) {
+                p.ids[t * p.k + sub + LPT] = i1;
+                p.weights[t * p.k + sub + LPT] = s1 * f;
+                atomicAdd(&hist[i1], 1);
+            }
+        }
+        unsigned again = __ballot_sync(kAll, real && open && sub == 0);
+        while (again) {
+            const int w = __ffs(again) - 1;
+            again &= again - 1;
+            exact_token<T, LPT * VPL / 32 ? LPT * VPL / 32 : 1>(p, tb + w / LPT, lane, hist);
+        }
+    }
+    __syncthreads();
+    for (int e = threadIdx.x; e < p.E; e += blockDim.x) {
+        if (one_block)
+            p.counts[e] = hist[e];
+        else if (hist[e])
+            atomicAdd(&p.counts[e], hist[e]);
+    }
+}
+
 template <typename T>
 cudaError_t launch_t(cudaStream_t s, int num_sms, const GateArgs& p) {
-    int64_t blocks = (p.n + kWarps - 1) / kWarps;
-    // up to two tokens a warp in one block: it overwrites the counts, and the clearing launch is saved
-    const int one = p.n <= 2 * kWarps;
-    if (one) blocks = 1;
-    if (!one) {
+    const int lpt = p.E <= 32 ? 4 : p.E <= 64 ? 8 : p.E <= 128 ? 16 : 32;
+    const int vpl = p.E <= 256 ? 8 : 16;
+    const int size = p.E / p.n_groups, q = size / vpl;
+    const bool lanes = p.E <= 512 && p.k <= 2 * lpt && (p.n_groups == 1 || (size % vpl == 0 && (q & (q - 1)) == 0));
+    const int tokens = kWarps * (lanes ? 32 / lpt : 1);      // a block's tokens at a time
+    int64_t blocks = (p.n + tokens - 1) / tokens;
+    // up to two rounds of one block: it overwrites the counts, and the clearing launch is saved
+    const int one = blocks <= 2;
+    if (one) {
+        blocks = 1;
+    } else {
         cudaError_t e = cudaMemsetAsync(p.counts, 0, p.E * sizeof(int32_t), s);
         if (e != cudaSuccess) return e;
     }
     if (blocks > (int64_t)num_sms * 16) blocks = (int64_t)num_sms * 16;
     const size_t smem = p.E * sizeof(int);
-#define CLHA_GATE(V) route_gated_kernel<T, V><<<(unsigned)blocks, kWarps * 32, smem, s>>>(p, one)
-    if (p.E <= 32) CLHA_GATE(1);
-    else if (p.E <= 64) CLHA_GATE(2);
-    else if (p.E <= 128) CLHA_GATE(4);
-    else if (p.E <= 256) CLHA_GATE(8);
-    else if (p.E <= 512) CLHA_GATE(16);
-    else CLHA_GATE(32);
+    if (lanes) {
+        const int vec = p.E % 8 == 0 && ((uintptr_t)p.logits & 15) == 0;
+#define CLHA_GATE(L, V) route_lanes_kernel<T, L, V><<<(unsigned)blocks, kWarps * 32, smem, s>>>(p, one, vec)
+        if (p.E <= 32) CLHA_GATE(4, 8);
+        else if (p.E <= 64) CLHA_GATE(8, 8);
+        else if (p.E <= 128) CLHA_GATE(16, 8);
+        else if (p.E <= 256) CLHA_GATE(32, 8);
+        else CLHA_GATE(32, 16);
 #undef CLHA_GATE
+    } else {
+#define CLHA_GATE(V) route_gated_kernel<T, V><<<(unsigned)blocks, kWarps * 32, smem, s>>>(p, one)
+        if (p.E <= 32) CLHA_GATE(1);
+        else if (p.E <= 64) CLHA_GATE(2);
+        else if (p.E <= 128) CLHA_GATE(4);
+        else if (p.E <= 256) CLHA_GATE(8);
+        else if (p.E <= 512) CLHA_GATE(16);
+        else CLHA_GATE(32);
+#undef CLHA_GATE
+    }
     clha_note_launches(1);
     return cudaGetLastError();
 }
