@@ -63,8 +63,6 @@ __device__ __forceinline__ F warp_max(F v) {
     }
     return v;
 }
-__device__ __forceinline__ float exp_of(float x) { return expf(x); }
-__device__ __forceinline__ double exp_of(double x) { return exp(x); }
 
 // Largest (value, lowest index) over the warp; index 0x7fffffff: none.
 template <typename F>
@@ -83,64 +81,62 @@ __device__ __forceinline__ void warp_best(F& v, int& i) {
 // 0.37 2^-24 through the exponential, as much through the sum, whose up to 37 roundings add 37 2^-24, and 2^-22
 // through the division and the product. A biased choice adds 2^-24 of its size. Twice that for the two.
 // (Sums of two are off by twice as much and a rounding of their own: three times the bound.)
-template <typename F>
-__device__ __forceinline__ F choice_slack(bool sigmoid, F top_score, F largest_choice) {
-    return (sigmoid ? (F)0x1p-21f : (F)0x1p-17f * top_score) + (F)0x1p-23f * largest_choice;
+__device__ __forceinline__ float choice_slack(bool sigmoid, float top_score, float largest_choice) {
+    return (sigmoid ? 0x1p-21f : 0x1p-17f * top_score) + 0x1p-23f * largest_choice;
 }
 
-// One token's selection in the arithmetic of F. Lane j < k (and j + 32, ...) writes the j-th expert and its
+// One token's selection by a warp, in float32. Lane j < k (and j + 32, ...) writes the j-th expert and its
 // weight. Returns false, with nothing written, where a decision was nearer than the error bound.
-template <typename F, int VPL>
+template <int VPL>
 __device__ __forceinline__ bool select_token(const GateArgs& p, const float (&l)[VPL], int64_t t, int lane, int* hist) {
-    constexpr bool kExact = sizeof(F) == 8;
     const bool by_logit = !p.bias && (p.n_groups == 1 || !p.top2);
-    F s[VPL], c[VPL];
-    F m = -INFINITY;
+    float s[VPL], c[VPL];
+    float m = -INFINITY;
 #pragma unroll
     for (int i = 0; i < VPL; ++i)
-        if (lane + 32 * i < p.E) m = l[i] > m ? (F)l[i] : m;
-    F top_score = 1;
+        if (lane + 32 * i < p.E) m = l[i] > m ? l[i] : m;
+    float top_score = 1;
     if (!p.sigmoid) {
         m = warp_max(m);
-        F sum = 0;
+        float sum = 0;
 #pragma unroll
         for (int i = 0; i < VPL; ++i) {
-            s[i] = lane + 32 * i < p.E ? exp_of((F)l[i] - m) : (F)0;
+            s[i] = lane + 32 * i < p.E ? expf(l[i] - m) : 0;
             sum += s[i];
         }
         sum = warp_sum(sum);
 #pragma unroll
         for (int i = 0; i < VPL; ++i) s[i] = s[i] / sum;
-        top_score = (F)1 / sum;
+        top_score = 1 / sum;
     } else {
 #pragma unroll
-        for (int i = 0; i < VPL; ++i) s[i] = lane + 32 * i < p.E ? (F)1 / ((F)1 + exp_of(-(F)l[i])) : (F)0;
+        for (int i = 0; i < VPL; ++i) s[i] = lane + 32 * i < p.E ? 1 / (1 + expf(-l[i])) : 0;
     }
     unsigned live = 0;   // bit i: expert lane + 32 i may be chosen
-    F big = 0;
+    float big = 0;
 #pragma unroll
     for (int i = 0; i < VPL; ++i) {
         const int e = lane + 32 * i;
-        c[i] = by_logit ? (F)l[i] : s[i];
+        c[i] = by_logit ? l[i] : s[i];
         if (e < p.E) {
             live |= 1u << i;
             if (p.bias) {
                 const float b = __ldg(p.bias + e);
                 if (isfinite(b))
-                    c[i] += (F)b;
+                    c[i] += b;
                 else                                          // recorded; taken as 0
                     clha_record_error(p.err, CLHA_ERR_NONFINITE, (int)(t & 0x7fffffff), e, KID_GATE);
-                big = fabs(c[i]) > big ? (F)fabs(c[i]) : big;
+                big = fabsf(c[i]) > big ? fabsf(c[i]) : big;
             }
         }
     }
-    F slack = 0;
-    if (!kExact && !by_logit) slack = choice_slack(p.sigmoid != 0, top_score, warp_max(big));
+    float slack = 0;
+    if (!by_logit) slack = choice_slack(p.sigmoid != 0, top_score, warp_max(big));
 
     if (p.n_groups > 1) {
         // rank every group (all lanes hold it), then keep the first top_groups
         const int size = p.E / p.n_groups;
-        F rank[VPL];     // lane holds groups lane, lane + 32, ...
+        float rank[VPL];     // lane holds groups lane, lane + 32, ...
         unsigned open = 0;
 #pragma unroll
         for (int i = 0; i < VPL; ++i) {
@@ -148,7 +144,7 @@ __device__ __forceinline__ bool select_token(const GateArgs& p, const float (&l)
             if (lane + 32 * i < p.n_groups) open |= 1u << i;
         }
         for (int g = 0; g < p.n_groups; ++g) {
-            F a = -INFINITY, b = -INFINITY;
+            float a = -INFINITY, b = -INFINITY;
 #pragma unroll
             for (int i = 0; i < VPL; ++i) {
                 const int e = lane + 32 * i;
@@ -158,28 +154,28 @@ __device__ __forceinline__ bool select_token(const GateArgs& p, const float (&l)
             }
 #pragma unroll
             for (int o = 16; o; o >>= 1) {   // the two largest of two pairs
-                const F oa = __shfl_xor_sync(kAll, a, o), ob = __shfl_xor_sync(kAll, b, o);
-                const F lo = a < oa ? a : oa;
+                const float oa = __shfl_xor_sync(kAll, a, o), ob = __shfl_xor_sync(kAll, b, o);
+                const float lo = a < oa ? a : oa;
                 a = a < oa ? oa : a;
                 b = b < ob ? ob : b;
                 b = b < lo ? lo : b;
             }
-            const F r = p.top2 && size > 1 ? a + b : a;
+            const float r = p.top2 && size > 1 ? a + b : a;
 #pragma unroll
             for (int i = 0; i < VPL; ++i)
                 if (g == lane + 32 * i) rank[i] = r;
         }
         unsigned kept = 0;
-        F last = 0;
+        float last = 0;
         for (int r = 0; r <= p.top_groups && r < p.n_groups; ++r) {
-            F bv = 0;
+            float bv = 0;
             int bi = 0x7fffffff;
 #pragma unroll
             for (int i = 0; i < VPL; ++i)
                 if ((open >> i & 1) && (bi == 0x7fffffff || rank[i] > bv)) { bv = rank[i]; bi = lane + 32 * i; }
             warp_best(bv, bi);
             if (r == p.top_groups) {
-                if (!kExact && !by_logit && last - bv <= 3 * slack) return false;
+                if (!by_logit && last - bv <= 3 * slack) return false;
                 break;
             }
             last = bv;
@@ -193,22 +189,22 @@ __device__ __forceinline__ bool select_token(const GateArgs& p, const float (&l)
         }
     }
 
-    F sum = 0, last = 0;
+    float sum = 0, last = 0;
     int my_id[VPL];
-    F my_s[VPL];
+    float my_s[VPL];
     bool open_order = false;
     for (int r = 0; r <= p.k; ++r) {
-        F bv = 0;
+        float bv = 0;
         int bi = 0x7fffffff;
 #pragma unroll
         for (int i = 0; i < VPL; ++i)
             if ((live >> i & 1) && (bi == 0x7fffffff || c[i] > bv)) { bv = c[i]; bi = lane + 32 * i; }
         warp_best(bv, bi);
         if (bi == 0x7fffffff) break;
-        if (!kExact && !by_logit && r > 0 && last - bv <= slack) open_order = true;
+        if (!by_logit && r > 0 && last - bv <= slack) open_order = true;
         if (r == p.k || open_order) break;
         last = bv;
-        F sv = 0;
+        float sv = 0;
 #pragma unroll
         for (int i = 0; i < VPL; ++i)
             if (i == bi >> 5) sv = s[i];
@@ -220,19 +216,151 @@ __device__ __forceinline__ bool select_token(const GateArgs& p, const float (&l)
             if (r == lane + 32 * i) { my_id[i] = bi; my_s[i] = sv; }
     }
     if (open_order) return false;
-    if (!kExact && p.renorm && !(sum > (F)1e-30f)) return false;   // float32 scores that underflow
+    if (p.renorm && !(sum > 1e-30f)) return false;   // float32 scores that underflow
 #pragma unroll
     for (int i = 0; i < VPL; ++i) {
         const int j = lane + 32 * i;
         if (j < p.k) {
-            F w = my_s[i];
-            if (p.renorm) w = sum > 0 ? w / sum : (F)1 / p.k;
+            float w = my_s[i];
+            if (p.renorm) w = sum > 0 ? w / sum : 1 / p.k;
             p.ids[t * p.k + j] = my_id[i];
-            p.weights[t * p.k + j] = (float)(w * (F)p.scale);
+            p.weights[t * p.k + j] = (float)(w * p.scale);
             atomicAdd(&hist[my_id[i]], 1);
         }
     }
     return true;
+}
+
+template <typename T>
+__device__ __forceinline__ float finite_logit(const T* row, int e) {
+    const float l = load_logit<T>(row, e);
+    return isfinite(l) ? l : 0.f;
+}
+
+// ------------------------------------------------------------------ the selection in float64
+// Taken by a warp for a token whose float32 choices leave a decision open: a token in thousands, but its
+// latency is the kernel's tail, so the doubles are compared as ordered 64-bit integers, whose warp-wide
+// maximum is two integer reductions (9973 x 256 experts with one such token: 24 us more as a selection by
+// exchanged doubles, EXACT_TAIL this way).
+__device__ __forceinline__ uint64_t to_key(double v) {        // larger value, larger key; never 0
+    const int64_t b = __double_as_longlong(v + 0.0);          // one zero
+    return b < 0 ? ~(uint64_t)b : (uint64_t)b | 0x8000000000000000ull;
+}
+__device__ __forceinline__ double from_key(uint64_t k) {
+    return __longlong_as_double(k >> 63 ? (int64_t)(k & 0x7fffffffffffffffull) : ~(int64_t)k);
+}
+__device__ __forceinline__ uint64_t warp_max_key(uint64_t k) {
+    const uint32_t hi = __reduce_max_sync(kAll, (uint32_t)(k >> 32));
+    const uint32_t lo = __reduce_max_sync(kAll, (uint32_t)(k >> 32) == hi ? (uint32_t)k : 0u);
+    return (uint64_t)hi << 32 | lo;
+}
+// The largest key over the warp and the lowest index 32 i + lane that holds it, among those that `in` admits.
+template <int N, typename In>
+__device__ __forceinline__ uint64_t best_key(const uint64_t (&key)[N], int lane, In in, int& index) {
+    uint64_t m = 0;
+#pragma unroll
+    for (int i = 0; i < N; ++i)
+        if (in(i) && key[i] > m) m = key[i];
+    m = warp_max_key(m);
+    unsigned at = 0xffffffffu;
+#pragma unroll
+    for (int i = N - 1; i >= 0; --i)
+        if (in(i) && key[i] == m) at = 32 * i + lane;
+    index = (int)__reduce_min_sync(kAll, at);
+    return m;
+}
+
+template <typename T, int VPL>
+__device__ __noinline__ void exact_token(const GateArgs& p, int64_t t, int lane, int* hist) {
+    const T* row = reinterpret_cast<const T*>(p.logits) + t * p.E;
+    double s[VPL];
+    uint64_t key[VPL];
+    float l[VPL], m = -INFINITY;
+#pragma unroll
+    for (int i = 0; i < VPL; ++i) {
+        l[i] = lane + 32 * i < p.E ? finite_logit<T>(row, lane + 32 * i) : -INFINITY;
+        m = fmaxf(m, l[i]);
+    }
+    m = warp_max(m);
+    double total = 1;
+#pragma unroll
+    for (int i = 0; i < VPL; ++i) s[i] = exp(p.sigmoid ? -(double)l[i] : (double)l[i] - (double)m);
+    if (!p.sigmoid) {
+        total = 0;
+#pragma unroll
+        for (int i = 0; i < VPL; ++i) total += s[i];
+        total = warp_sum(total);
+    }
+    const bool by_logit = !p.bias && (p.n_groups == 1 || !p.top2);
+#pragma unroll
+    for (int i = 0; i < VPL; ++i) {
+        const int e = lane + 32 * i;
+        s[i] = p.sigmoid ? 1 / (1 + s[i]) : s[i] / total;
+        key[i] = 0;
+        if (e < p.E) {
+            const float b = p.bias ? __ldg(p.bias + e) : 0.f;
+            key[i] = to_key(by_logit ? (double)l[i] : isfinite(b) ? s[i] + (double)b : s[i]);
+        }
+    }
+    if (p.n_groups > 1) {
+        const int size = p.E / p.n_groups;
+        uint64_t rank[VPL];                                   // of groups lane, lane + 32, ...
+#pragma unroll
+        for (int i = 0; i < VPL; ++i) rank[i] = 0;
+        for (int g = 0; g < p.n_groups; ++g) {
+            int first, second;
+            const auto inside = [&](int i) { return (unsigned)(lane + 32 * i - g * size) < (unsigned)size; };
+            uint64_t r = best_key(key, lane, inside, first);
+            if (p.top2 && size > 1) {
+                const uint64_t r2 =
+                    best_key(key, lane, [&](int i) { return inside(i) && lane + 32 * i != first; }, second);
+                r = to_key(from_key(r) + from_key(r2));
+            }
+#pragma unroll
+            for (int i = 0; i < VPL; ++i)
+                if (g == lane + 32 * i) rank[i] = r;
+        }
+        unsigned kept = 0;
+        for (int r = 0; r < p.top_groups; ++r) {
+            int g;
+            best_key(rank, lane, [](int) { return true; }, g);
+#pragma unroll
+            for (int i = 0; i < VPL; ++i)
+                if (g == lane + 32 * i) { rank[i] = 0; kept |= 1u << i; }
+        }
+#pragma unroll
+        for (int i = 0; i < VPL; ++i) {
+            const int e = lane + 32 * i, g = e < p.E ? e / size : 0;
+            const unsigned who = __shfl_sync(kAll, kept, g & 31);
+            if (!(who >> (g >> 5) & 1)) key[i] = 0;
+        }
+    }
+    double sum = 0;
+    int my_id[VPL];
+    double my_s[VPL];
+    for (int r = 0; r < p.k; ++r) {
+        int e;
+        best_key(key, lane, [](int) { return true; }, e);
+        double sv = 0;
+#pragma unroll
+        for (int i = 0; i < VPL; ++i)
+            if (e == lane + 32 * i) { key[i] = 0; sv = s[i]; }
+        sv = __shfl_sync(kAll, sv, e & 31);
+        sum += sv;
+#pragma unroll
+        for (int i = 0; i < VPL; ++i)
+            if (r == lane + 32 * i) { my_id[i] = e; my_s[i] = sv; }
+    }
+#pragma unroll
+    for (int i = 0; i < VPL; ++i) {
+        const int j = lane + 32 * i;
+        if (j < p.k) {
+            const double w = p.renorm ? (sum > 0 ? my_s[i] / sum : 1.0 / p.k) : my_s[i];
+            p.ids[t * p.k + j] = my_id[i];
+            p.weights[t * p.k + j] = (float)(w * (double)p.scale);
+            atomicAdd(&hist[my_id[i]], 1);
+        }
+    }
 }
 
 template <typename T, int VPL>
@@ -252,7 +380,7 @@ __global__ void __launch_bounds__(kWarps * 32) route_gated_kernel(GateArgs p, in
         }
         if (__any_sync(kAll, bad) && lane == 0)
             clha_record_error(p.err, CLHA_ERR_NONFINITE, (int)(t & 0x7fffffff), 0, KID_GATE);
-        if (!select_token<float, VPL>(p, l, t, lane, hist)) select_token<double, VPL>(p, l, t, lane, hist);
+        if (!select_token<VPL>(p, l, t, lane, hist)) exact_token<T, VPL>(p, t, lane, hist);
     }
     __syncthreads();
     for (int e = threadIdx.x; e < p.E; e += blockDim.x) {
@@ -264,10 +392,14 @@ __global__ void __launch_bounds__(kWarps * 32) route_gated_kernel(GateArgs p, in
 }
 
 // ------------------------------------------------------------------ LPT lanes a token, VPL experts a lane
-template <int LPT, typename F>
-__device__ __forceinline__ F lanes_max(F v) {
+template <int LPT>
+__device__ __forceinline__ float lanes_max(float v) {
+    if (LPT == 32) {
+        asm("redux.sync.max.f32 %0, %0, 0xffffffff;" : "+f"(v));
+    } else {
 #pragma unroll
-    for (int o = LPT / 2; o; o >>= 1) v = fmaxf(v, __shfl_xor_sync(kAll, v, o));
+        for (int o = LPT / 2; o; o >>= 1) v = fmaxf(v, __shfl_xor_sync(kAll, v, o));
+    }
     return v;
 }
 template <int LPT>
@@ -298,21 +430,8 @@ __device__ __forceinline__ void load_run(const T* p, float (&l)[VPL]) {   // 16-
     }
 }
 
-// Where a token needs float64: the whole warp takes it, as the general kernel would.
-template <typename T, int WPL>
-__device__ __noinline__ void exact_token(const GateArgs& p, int64_t t, int lane, int* hist) {
-    float l[WPL];
-#pragma unroll
-    for (int i = 0; i < WPL; ++i) {
-        const int e = lane + 32 * i;
-        l[i] = e < p.E ? load_logit<T>(p.logits, t * p.E + e) : 0.f;
-        if (!isfinite(l[i])) l[i] = 0.f;
-    }
-    select_token<double, WPL>(p, l, t, lane, hist);
-}
-
 template <typename T, int LPT, int VPL>
-__global__ void __launch_bounds__(kWarps * 32) route_lanes_kernel(GateArgs p, int one_block, int vec) {
+__global__ void __launch_bounds__(kWarps * 32, VPL == 8 ? 4 : 2) route_lanes_kernel(GateArgs p, int one_block, int vec) {
     constexpr int TPW = 32 / LPT;                            // tokens a warp
     extern __shared__ int hist[];
     for (int e = threadIdx.x; e < p.E; e += blockDim.x) hist[e] = 0;
@@ -337,7 +456,7 @@ __global__ void __launch_bounds__(kWarps * 32) route_lanes_kernel(GateArgs p, in
          tb += (int64_t)gridDim.x * per_block) {
         const int64_t t = tb + lane / LPT;
         const bool real = t < p.n;
-        float c[VPL], s[VPL];
+        float c[VPL];
         const T* row = reinterpret_cast<const T*>(p.logits) + (real ? t : 0) * p.E;
         if (vec && e0 + VPL <= p.E) {
             load_run<T, VPL>(row + e0, c);
@@ -345,38 +464,34 @@ __global__ void __launch_bounds__(kWarps * 32) route_lanes_kernel(GateArgs p, in
 #pragma unroll
             for (int i = 0; i < VPL; ++i) c[i] = e0 + i < p.E ? load_logit<T>(row, e0 + i) : -INFINITY;
         }
+        float m = 0.f, top_score = 1.f;
         bool bad = false;
 #pragma unroll
         for (int i = 0; i < VPL; ++i)
             if (e0 + i < p.E && !isfinite(c[i])) { bad = true; c[i] = 0.f; }   // recorded; the ids stay in range
         if (bad && real) clha_record_error(p.err, CLHA_ERR_NONFINITE, (int)(t & 0x7fffffff), 0, KID_GATE);
-
-        float top_score = 1.f;
         if (!p.sigmoid) {
-            float m = c[0], sum = 0.f;
+            m = c[0];
+            float sum = 0.f;
 #pragma unroll
             for (int i = 1; i < VPL; ++i) m = fmaxf(m, c[i]);
             m = lanes_max<LPT>(m);
 #pragma unroll
-            for (int i = 0; i < VPL; ++i) {
-                s[i] = expf(c[i] - m);                       // past E: exp(-inf) = 0
-                sum += s[i];
-            }
+            for (int i = 0; i < VPL; ++i) sum += expf(c[i] - m);   // past E: exp(-inf) = 0
             top_score = 1.f / lanes_sum<LPT>(sum);
-#pragma unroll
-            for (int i = 0; i < VPL; ++i) s[i] *= top_score;
-        } else {
-#pragma unroll
-            for (int i = 0; i < VPL; ++i) s[i] = 1.f / (1.f + expf(-c[i]));
         }
+        const auto score = [&](float l) {
+            return p.sigmoid ? __fdividef(1.f, 1.f + expf(-l)) : expf(l - m) * top_score;
+        };
         float slack = 0.f;
         if (!by_logit) {
             float big = 0.f;
 #pragma unroll
-            for (int i = 0; i < VPL; ++i) {
-                c[i] = e0 + i < p.E ? (p.bias ? s[i] + bias[i] : s[i]) : -INFINITY;
-                if (e0 + i < p.E) big = fmaxf(big, fabsf(c[i]));
-            }
+            for (int i = 0; i < VPL; ++i)
+                if (e0 + i < p.E) {
+                    c[i] = score(c[i]) + (p.bias ? bias[i] : 0.f);
+                    big = fmaxf(big, fabsf(c[i]));
+                }
             slack = choice_slack(p.sigmoid != 0, top_score, lanes_max<LPT>(big));
         }
         bool open = false;                                   // a decision inside the error bound
@@ -397,17 +512,14 @@ __global__ void __launch_bounds__(kWarps * 32) route_lanes_kernel(GateArgs p, in
             const float rank = !in ? -INFINITY : p.top2 ? a + b : a;
             const int g = sub / q;
             int ahead = 0;
-            float above = INFINITY, below = -INFINITY;       // the last kept and the first dropped rank
             for (int h = 0; h < p.n_groups; ++h) {
                 const float r = __shfl_sync(kAll, rank, first + h * q);
                 ahead += r > rank || (r == rank && h < g);
             }
             const bool kept = in && ahead < p.top_groups;
-            if (!by_logit && p.top_groups < p.n_groups) {
-                if (in && kept) above = rank;
-                if (in && !kept) below = rank;
-                above = -lanes_max<LPT>(-above);
-                below = lanes_max<LPT>(below);
+            if (!by_logit && p.top_groups < p.n_groups) {    // the last kept and the first dropped rank
+                const float above = -lanes_max<LPT>(in && kept ? -rank : -INFINITY);
+                const float below = lanes_max<LPT>(in && !kept ? rank : -INFINITY);
                 open = above - below <= 3 * slack;
             }
             if (!kept) {
@@ -415,47 +527,45 @@ __global__ void __launch_bounds__(kWarps * 32) route_lanes_kernel(GateArgs p, in
                 for (int i = 0; i < VPL; ++i) c[i] = -INFINITY;
             }
         }
-        float sum = 0.f, last = INFINITY, s0 = 0.f, s1 = 0.f;
-        int i0 = 0, i1 = 0;
+        float last = INFINITY;
+        int id0 = 0, id1 = 0;                                // this lane's choices: the sub-th and the (sub + LPT)-th
         const int rounds = by_logit ? p.k : p.k + 1;         // one more, to see how near the first loser is
         for (int r = 0; r < rounds; ++r) {
-            float m = c[0];
+            float mx = c[0];
 #pragma unroll
-            for (int i = 1; i < VPL; ++i) m = fmaxf(m, c[i]);
-            const float best = lanes_max<LPT>(m);
-            if (!by_logit && r > 0 && last - best <= slack) open = true;
-            if (r == p.k) break;
+            for (int i = 1; i < VPL; ++i) mx = fmaxf(mx, c[i]);
+            const float best = lanes_max<LPT>(mx);
+            if (last - best <= slack && !by_logit) open = true;
             last = best;
-            const unsigned who = __ballot_sync(kAll, m == best) & mine;
-            const int owner = __ffs(who) - 1;
+            const int owner = __ffs(__ballot_sync(kAll, mx == best) & mine) - 1;
             int idx = 0;
-            float sv = 0.f;
 #pragma unroll
-            for (int i = VPL - 1; i >= 0; --i)               // the first of the lane's values that is the largest
-                if (c[i] == m) { idx = i; sv = s[i]; }
-            if (owner == lane) {
+            for (int i = VPL - 1; i >= 0; --i) idx = c[i] == best ? i : idx;   // the first that is the largest
+            const int gone = owner == lane ? idx : -1;
 #pragma unroll
-                for (int i = 0; i < VPL; ++i)
-                    if (i == idx) c[i] = -INFINITY;
-            }
+            for (int i = 0; i < VPL; ++i) c[i] = i == gone ? -INFINITY : c[i];
             const int e = __shfl_sync(kAll, e0 + idx, owner);
-            sv = __shfl_sync(kAll, sv, owner);
-            sum += sv;
-            if (r == sub) { i0 = e; s0 = sv; }
-            if (r == sub + LPT) { i1 = e; s1 = sv; }
+            id0 = r == sub ? e : id0;
+            id1 = r == sub + LPT ? e : id1;
         }
-        if (p.renorm && !(sum > 1e-30f)) open = true;        // float32 scores that underflow
+        const bool has0 = sub < p.k, has1 = sub + LPT < p.k;
+        const float s0 = has0 ? score(finite_logit<T>(row, id0)) : 0.f, s1 = has1 ? score(finite_logit<T>(row, id1)) : 0.f;
+        float f = p.scale;
+        if (p.renorm) {
+            const float sum = lanes_sum<LPT>(s0 + s1);
+            if (!(sum > 1e-30f)) open = true;                // float32 scores that underflow
+            f = p.scale / sum;
+        }
         if (real && !open) {
-            const float f = p.renorm ? p.scale / sum : p.scale;
-            if (sub < p.k) {
-                p.ids[t * p.k + sub] = i0;
+            if (has0) {
+                p.ids[t * p.k + sub] = id0;
                 p.weights[t * p.k + sub] = s0 * f;
-                atomicAdd(&hist[i0], 1);
+                atomicAdd(&hist[id0], 1);
             }
-            if (sub + LPT < p.k) {
-                p.ids[t * p.k + sub + LPT] = i1;
+            if (has1) {
+                p.ids[t * p.k + sub + LPT] = id1;
                 p.weights[t * p.k + sub + LPT] = s1 * f;
-                atomicAdd(&hist[i1], 1);
+                atomicAdd(&hist[id1], 1);
             }
         }
         unsigned again = __ballot_sync(kAll, real && open && sub == 0);
@@ -490,7 +600,9 @@ cudaError_t launch_t(cudaStream_t s, int num_sms, const GateArgs& p) {
         cudaError_t e = cudaMemsetAsync(p.counts, 0, p.E * sizeof(int32_t), s);
         if (e != cudaSuccess) return e;
     }
-    if (blocks > (int64_t)num_sms * 16) blocks = (int64_t)num_sms * 16;
+    // one wave: a block's histogram and bias serve all of its tokens
+    const int64_t wave = (int64_t)num_sms * (lanes ? 4 : 8);
+    if (blocks > wave) blocks = wave;
     const size_t smem = p.E * sizeof(int);
     if (lanes) {
         const int vec = p.E % 8 == 0 && ((uintptr_t)p.logits & 15) == 0;
