@@ -12,9 +12,12 @@
 // (borders have at most 5 bits, so x and border * s * g differ by 2^-33 of their size or not at all).
 // A power-of-two scale without g needs no quotient: x times a power of two is exact.
 //
-// Both kernels stream: a warp takes 256 columns of the four rows r, r + 32, r + 64, r + 96 of a 128-row
-// tile (four loads in flight a lane), because those rows' scales of four blocks are 16 consecutive bytes
-// of the tiled scale layout and leave in one store.
+// Both kernels stream. Eight lanes take 128 columns, 16 a lane (32 bytes of bf16 in one access, 8 bytes of
+// codes), of the four rows r, r + 32, r + 64, r + 96 of a 128-row tile: four loads in flight a lane, and the
+// scales of four blocks of those rows are 16 consecutive bytes of the tiled layout (the lanes transpose 4 x 4
+// bytes by two exchanges and store 4 bytes each). A block is one lane (16) or two (32). With 8 columns a lane, a
+// 64-bit division a step and byte-wise decoding the kernels were issue-bound: 32768 tokens x 2048 into the segments
+// of 64 experts, top 6, took 285 us (114 instructions per 8 columns) and decoding to bf16 340 us.
 #include "clha_internal.h"
 
 #include <cuda_fp16.h>
@@ -25,7 +28,7 @@ constexpr float kLo = 1.f - 0x1p-21f, kHi = 1.f + 0x1p-21f;
 constexpr int kThreads = 256;
 
 // Eight e2m1 codes of v[0..7], v[0] in the low bits.
-__device__ __forceinline__ uint32_t e2m1x8(const float (&v)[8]) {
+__device__ __forceinline__ uint32_t e2m1x8(const float* v) {
     uint32_t r;
     asm("{\n\t.reg .b8 a, b, c, d;\n\t"
         "cvt.rn.satfinite.e2m1x2.f32 a, %2, %1;\n\t"
@@ -35,6 +38,19 @@ __device__ __forceinline__ uint32_t e2m1x8(const float (&v)[8]) {
         "mov.b32 %0, {a, b, c, d};\n\t}"
         : "=r"(r) : "f"(v[0]), "f"(v[1]), "f"(v[2]), "f"(v[3]), "f"(v[4]), "f"(v[5]), "f"(v[6]), "f"(v[7]));
     return r;
+}
+// The eight numbers of a word of codes, as four pairs of halves (exact).
+__device__ __forceinline__ void from_e2m1x8(uint32_t q, __half2 (&v)[4]) {
+    uint32_t o[4];
+    asm("{\n\t.reg .b8 a, b, c, d;\n\t"
+        "mov.b32 {a, b, c, d}, %4;\n\t"
+        "cvt.rn.f16x2.e2m1x2 %0, a;\n\t"
+        "cvt.rn.f16x2.e2m1x2 %1, b;\n\t"
+        "cvt.rn.f16x2.e2m1x2 %2, c;\n\t"
+        "cvt.rn.f16x2.e2m1x2 %3, d;\n\t}"
+        : "=r"(o[0]), "=r"(o[1]), "=r"(o[2]), "=r"(o[3]) : "r"(q));
+#pragma unroll
+    for (int i = 0; i < 4; ++i) v[i] = *reinterpret_cast<__half2*>(&o[i]);
 }
 // e4m3 codes of two floats, the first in the low byte.
 __device__ __forceinline__ uint32_t e4m3x2(float a, float b) {
@@ -70,24 +86,49 @@ __device__ __noinline__ uint32_t e2m1_exact(float x, double d) {
     return c | (signbit(x) ? 8u : 0u);
 }
 
-template <typename T>
-__device__ __forceinline__ void load8(const T* p, float (&v)[8]);
-template <>
-__device__ __forceinline__ void load8<float>(const float* p, float (&v)[8]) {
-    const float4 a = __ldcs(reinterpret_cast<const float4*>(p)), b = __ldcs(reinterpret_cast<const float4*>(p) + 1);
-    v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
-    v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
-}
-template <>
-__device__ __forceinline__ void load8<__nv_bfloat16>(const __nv_bfloat16* p, float (&v)[8]) {
-    const uint4 a = __ldg(reinterpret_cast<const uint4*>(p));
-    const uint32_t w[4] = {a.x, a.y, a.z, a.w};
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        v[2 * i] = __uint_as_float(w[i] << 16);
-        v[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+// 32 bytes at a time: one access where the address is a multiple of 32 (`wide`), two where it is one of 16.
+__device__ __forceinline__ void load32(const void* p, bool wide, uint32_t (&w)[8]) {
+    if (wide) {
+        asm volatile("ld.global.nc.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+                     : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]), "=r"(w[4]), "=r"(w[5]), "=r"(w[6]), "=r"(w[7])
+                     : "l"(p));
+    } else {
+        const uint4 a = __ldg(reinterpret_cast<const uint4*>(p)), b = __ldg(reinterpret_cast<const uint4*>(p) + 1);
+        w[0] = a.x; w[1] = a.y; w[2] = a.z; w[3] = a.w;
+        w[4] = b.x; w[5] = b.y; w[6] = b.z; w[7] = b.w;
     }
 }
+__device__ __forceinline__ void store32(void* p, bool wide, const uint32_t (&w)[8]) {
+    if (wide) {
+        asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};"
+                     ::"l"(p), "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
+                     : "memory");
+    } else {
+        reinterpret_cast<uint4*>(p)[0] = make_uint4(w[0], w[1], w[2], w[3]);
+        reinterpret_cast<uint4*>(p)[1] = make_uint4(w[4], w[5], w[6], w[7]);
+    }
+}
+
+// Sixteen columns as they lie in memory, and as floats.
+template <typename T>
+struct Raw {
+    static constexpr int N = (int)sizeof(T) / 2;             // accesses of 32 bytes
+    uint32_t w[N][8];
+    __device__ __forceinline__ void load(const T* p, bool wide) {
+#pragma unroll
+        for (int i = 0; i < N; ++i) load32(reinterpret_cast<const char*>(p) + 32 * i, wide, w[i]);
+    }
+    __device__ __forceinline__ void zero() {
+#pragma unroll
+        for (int i = 0; i < N; ++i)
+#pragma unroll
+            for (int j = 0; j < 8; ++j) w[i][j] = 0;
+    }
+    __device__ __forceinline__ float at(int i) const {       // i a constant once unrolled
+        if (sizeof(T) == 4) return __uint_as_float(w[i >> 3 & (N - 1)][i & 7]);
+        return __uint_as_float(i & 1 ? w[0][i >> 1] & 0xffff0000u : w[0][i >> 1] << 16);
+    }
+};
 
 // The block scale's byte for the largest magnitude `top` (finite) of a block, and *r ~ 1 / (s g).
 template <int BLOCK, bool SCALED>
@@ -124,6 +165,28 @@ __device__ __forceinline__ uint32_t block_scale(float top, float g, float rg, fl
     return byte;
 }
 
+// The work items: 128 columns of four rows, item = slot * chunks + chunk with 32 slots a 128-row tile. Eight
+// lanes take one, and go on in steps of all groups of eight; no division after the first item.
+struct Items {
+    int64_t slot;
+    int chunk;
+    int64_t step_slot;
+    int step_chunk, chunks;
+    __device__ __forceinline__ Items(int chunks_) : chunks(chunks_) {
+        const int64_t groups = (int64_t)gridDim.x * (kThreads / 8);
+        const int64_t id = (int64_t)blockIdx.x * (kThreads / 8) + (threadIdx.x >> 3);
+        slot = id / chunks;
+        chunk = (int)(id - slot * chunks);
+        step_slot = groups / chunks;
+        step_chunk = (int)(groups - step_slot * chunks);
+    }
+    __device__ __forceinline__ void next() {
+        slot += step_slot;
+        chunk += step_chunk;
+        if (chunk >= chunks) { chunk -= chunks; ++slot; }
+    }
+};
+
 // ------------------------------------------------------------------------------ quantization
 struct QuantArgs {
     const void* X;
@@ -136,39 +199,41 @@ struct QuantArgs {
     int64_t rows_per_g;
     uint8_t* codes;
     uint8_t* scales;
-    int64_t items;                // 128-row tiles * 32 * column chunks
-    int chunks;                   // of 256 columns
+    int wide;                     // X is 32-byte aligned
     int* err;
 };
 
 template <typename T, int BLOCK, bool SCALED>
 __global__ void __launch_bounds__(kThreads) fp4_quantize_kernel(QuantArgs p) {
-    const int lane = threadIdx.x & 31;
-    const int64_t warps = (int64_t)gridDim.x * (kThreads / 32);
+    const int lane = threadIdx.x & 31, sub = lane & 7;
     const int64_t live = p.seg ? p.seg[p.E] : p.rows;
-    constexpr int LPB = BLOCK / 8;                           // lanes a block
+    const int64_t slots = (min(live, p.rows) + 127) / 128 * 32;
+    constexpr int LPB = BLOCK / 16;                          // lanes a block
     const int atoms = p.d / BLOCK / 4;                       // 512-byte scale tiles across a row tile
-    for (int64_t w = (int64_t)blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5); w < p.items; w += warps) {
-        const int64_t slot = w / p.chunks;                   // 32 per row tile
-        const int c = (int)(w - slot * p.chunks) * 256 + lane * 8;
-        const int64_t r0 = (slot >> 5) * 128 + (slot & 31);
-        if ((slot >> 5) * 128 >= live) break;                // (w ascends)
-        const bool in_row = c < p.d;
-        float v[4][8];
+    Items it(p.d >> 7);
+    // whole warps leave together: the lanes of one exchange values
+    for (; __any_sync(0xffffffffu, it.slot < slots); it.next()) {
+        const bool work = it.slot < slots;
+        const int64_t r0 = (it.slot >> 5) * 128 + (it.slot & 31);
+        const int c = it.chunk * 128 + sub * 16;
+        Raw<T> x[4];
         bool has[4];
 #pragma unroll
         for (int a = 0; a < 4; ++a) {
             const int64_t row = r0 + 32 * a;
-            has[a] = in_row && row < live && row < p.rows;
+            has[a] = work && row < live && row < p.rows;
             int64_t src = row;
-            if (has[a] && p.perm) src = p.perm[row];
-            const bool real = has[a] && src >= 0 && src < p.n;
-            if (has[a] && src >= p.n) clha_record_error(p.err, CLHA_ERR_INVALID_ARG, (int)(row & 0x7fffffff), (int)src, KID_FP4);
-#pragma unroll
-            for (int i = 0; i < 8; ++i) v[a][i] = 0.f;
-            if (real) load8<T>(reinterpret_cast<const T*>(p.X) + src * p.d + c, v[a]);
+            if (p.perm) src = has[a] ? p.perm[row] : -1;
+            if (has[a] && src >= p.n) {
+                clha_record_error(p.err, CLHA_ERR_INVALID_ARG, (int)(row & 0x7fffffff), (int)src, KID_FP4);
+                src = -1;
+            }
+            if (has[a] && src >= 0)
+                x[a].load(reinterpret_cast<const T*>(p.X) + src * p.d + c, p.wide);
+            else
+                x[a].zero();
         }
-        uint32_t sb[4];
+        uint32_t sb = 0;                                     // the four rows' scale bytes of this lane's block
 #pragma unroll
         for (int a = 0; a < 4; ++a) {
             const int64_t row = r0 + 32 * a;
@@ -185,126 +250,147 @@ __global__ void __launch_bounds__(kThreads) fp4_quantize_kernel(QuantArgs p) {
             const float r6g = rg * (1.f / 6.f);
             float top = 0.f;
 #pragma unroll
-            for (int i = 0; i < 8; ++i) top = max_nan(top, fabsf(v[a][i]));
-#pragma unroll
-            for (int o = 1; o < LPB; o <<= 1) top = max_nan(top, __shfl_xor_sync(0xffffffffu, top, o));
-            uint32_t q;
-            if (!(top < INFINITY)) {                         // the same decision in all lanes of the block
+            for (int i = 0; i < 16; ++i) top = max_nan(top, fabsf(x[a].at(i)));
+            if (LPB == 2) top = max_nan(top, __shfl_xor_sync(0xffffffffu, top, 1));
+            uint32_t q[2] = {0u, 0u}, byte;
+            if (!(top < INFINITY)) {                         // the same decision in both lanes of a block
                 clha_record_error(p.err, CLHA_ERR_NONFINITE, (int)(row & 0x7fffffff), c, KID_FP4);
-                sb[a] = BLOCK == 32 ? 0xff : 0x7f;           // the formats' NaN
-                q = 0;
+                byte = BLOCK == 32 ? 0xff : 0x7f;            // the formats' NaN
             } else {
                 float r;
-                sb[a] = block_scale<BLOCK, SCALED>(top, g, rg, r6g, &r);
-                float lo[8];
-                if (BLOCK == 32 && !SCALED) {
+                byte = block_scale<BLOCK, SCALED>(top, g, rg, r6g, &r);
 #pragma unroll
-                    for (int i = 0; i < 8; ++i) lo[i] = v[a][i] * r;
-                    q = e2m1x8(lo);
-                } else {
-                    float hi[8];
+                for (int h = 0; h < 2; ++h) {
+                    float t[8];
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) t[i] = x[a].at(8 * h + i) * r;
+                    if (BLOCK == 32 && !SCALED) {
+                        q[h] = e2m1x8(t);
+                        continue;
+                    }
+                    float lo[8], hi[8];
 #pragma unroll
                     for (int i = 0; i < 8; ++i) {
-                        const float t = v[a][i] * r;
-                        lo[i] = t * kLo;
-                        hi[i] = t * kHi;
+                        lo[i] = t[i] * kLo;
+                        hi[i] = t[i] * kHi;
                     }
-                    q = e2m1x8(lo);
-                    if (q != e2m1x8(hi) || (r != 0.f && !(r > 0x1p-100f && r < 0x1p100f))) {
-                        const double dd = (BLOCK == 32 ? ldexp(1.0, (int)sb[a] - 127) : (double)from_e4m3(sb[a])) * (double)g;
-                        q = 0;
+                    q[h] = e2m1x8(lo);
+                    if (q[h] != e2m1x8(hi) || (r != 0.f && !(r > 0x1p-100f && r < 0x1p100f))) {
+                        const double dd = (BLOCK == 32 ? ldexp(1.0, (int)byte - 127) : (double)from_e4m3(byte)) * (double)g;
+                        q[h] = 0;
                         if (dd > 0.0)
 #pragma unroll
-                            for (int i = 0; i < 8; ++i) q |= e2m1_exact(v[a][i], dd) << (4 * i);
+                            for (int i = 0; i < 8; ++i) q[h] |= e2m1_exact(x[a].at(8 * h + i), dd) << (4 * i);
                     }
                 }
             }
-            if (has[a]) __stcs(reinterpret_cast<uint32_t*>(p.codes + row * (p.d / 2) + c / 2), q);
-            if (!has[a]) sb[a] = 0;
-            // the four blocks of this lane's scale cell, one byte each
-            const int kb = (lane / LPB) & 3;
-            uint32_t word = sb[a] << (8 * kb);
-            word |= __shfl_xor_sync(0xffffffffu, word, LPB);
-            word |= __shfl_xor_sync(0xffffffffu, word, 2 * LPB);
-            sb[a] = word;
+            if (has[a]) {
+                *reinterpret_cast<uint2*>(p.codes + row * (p.d >> 1) + (c >> 1)) = make_uint2(q[0], q[1]);
+                sb |= byte << (8 * a);
+            }
         }
-        if (in_row && lane % (4 * LPB) == 0)
-            *reinterpret_cast<uint4*>(p.scales + (((slot >> 5) * atoms + c / (4 * BLOCK)) * 32 + (slot & 31)) * 16) =
-                make_uint4(sb[0], sb[1], sb[2], sb[3]);
+        // lane b of a tile's four blocks holds the bytes of rows 0..3 (32 apart); exchange: it gets row b's four blocks
+        const int b = sub / LPB & 3;
+        uint32_t o = __shfl_xor_sync(0xffffffffu, sb, LPB);
+        sb = b & 1 ? __byte_perm(sb, o, 0x3715) : __byte_perm(sb, o, 0x6240);
+        o = __shfl_xor_sync(0xffffffffu, sb, 2 * LPB);
+        sb = b & 2 ? __byte_perm(sb, o, 0x3276) : __byte_perm(sb, o, 0x5410);
+        if (work && (LPB == 1 || !(sub & 1)))
+            *reinterpret_cast<uint32_t*>(p.scales + (((it.slot >> 5) * atoms + c / (4 * BLOCK)) * 32 + (it.slot & 31)) * 16 +
+                                         4 * b) = sb;
     }
+}
+
+// blocks for `items` of eight lanes: a few waves at most
+unsigned item_blocks(int64_t items, int num_sms) {
+    const int64_t blocks = (items + kThreads / 8 - 1) / (kThreads / 8), most = (int64_t)num_sms * 8;
+    return (unsigned)(blocks < most ? blocks : most);
 }
 
 template <typename T, int BLOCK>
 cudaError_t launch_q(cudaStream_t s, int num_sms, const QuantArgs& p) {
-    int64_t blocks = (p.items + kThreads / 32 - 1) / (kThreads / 32);
-    if (blocks > (int64_t)num_sms * 32) blocks = (int64_t)num_sms * 32;
+    const unsigned blocks = item_blocks((p.rows + 127) / 128 * 32 * (p.d >> 7), num_sms);
     if (p.g)
-        fp4_quantize_kernel<T, BLOCK, true><<<(unsigned)blocks, kThreads, 0, s>>>(p);
+        fp4_quantize_kernel<T, BLOCK, true><<<blocks, kThreads, 0, s>>>(p);
     else
-        fp4_quantize_kernel<T, BLOCK, false><<<(unsigned)blocks, kThreads, 0, s>>>(p);
+        fp4_quantize_kernel<T, BLOCK, false><<<blocks, kThreads, 0, s>>>(p);
     clha_note_launches(1);
     return cudaGetLastError();
 }
 
 // ------------------------------------------------------------------------------ decoding
 // q s g rounded once: q s is exact (6 bits) and float32's product with g is one rounding. A bfloat16 result
-// rounds the product towards zero first and keeps a sticky bit, so that it too is rounded once.
-__device__ __forceinline__ uint32_t bf16_once(float v, float g) {
-    float t = __fmul_rz(v, g);
-    if (__fmaf_rn(v, g, -t) != 0.f) t = __uint_as_float(__float_as_uint(t) | 1u);
-    return __bfloat16_as_ushort(__float2bfloat16_rn(t));
+// rounds the product towards zero first and keeps a sticky bit, so that it too is rounded once (without g it is
+// exact).
+__device__ __forceinline__ float sticky(float v, float g) {
+    const float t = __fmul_rz(v, g);
+    return __fmaf_rn(v, g, -t) != 0.f ? __uint_as_float(__float_as_uint(t) | 1u) : t;
+}
+__device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
+    uint32_t r;
+    asm("cvt.rn.bf16x2.f32 %0, %2, %1;" : "=r"(r) : "f"(a), "f"(b));
+    return r;
 }
 
-template <int BLOCK, bool F32>
+template <int BLOCK, bool F32, bool SCALED>
 __global__ void __launch_bounds__(kThreads) fp4_dequantize_kernel(const uint8_t* __restrict__ codes,
                                                                   const uint8_t* __restrict__ scales, int64_t rows, int d,
                                                                   const float* __restrict__ g, int64_t rows_per_g,
-                                                                  int64_t items, int chunks, void* __restrict__ out) {
-    const int lane = threadIdx.x & 31;
-    const int64_t warps = (int64_t)gridDim.x * (kThreads / 32);
+                                                                  int wide, void* __restrict__ out) {
+    const int sub = threadIdx.x & 7;
+    const int64_t slots = (rows + 127) / 128 * 32;
     const int atoms = d / BLOCK / 4;
-    for (int64_t w = (int64_t)blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5); w < items; w += warps) {
-        const int64_t slot = w / chunks;
-        const int c = (int)(w - slot * chunks) * 256 + lane * 8;
-        const int64_t r0 = (slot >> 5) * 128 + (slot & 31);
-        if (c >= d) continue;
-        uint32_t q[4] = {};
+    for (Items it(d >> 7); it.slot < slots; it.next()) {
+        const int64_t r0 = (it.slot >> 5) * 128 + (it.slot & 31);
+        const int c = it.chunk * 128 + sub * 16;
+        uint2 q[4];
         const uint4 sv = __ldg(reinterpret_cast<const uint4*>(
-            scales + (((slot >> 5) * atoms + c / (4 * BLOCK)) * 32 + (slot & 31)) * 16));
+            scales + (((it.slot >> 5) * atoms + c / (4 * BLOCK)) * 32 + (it.slot & 31)) * 16));
         const uint32_t sw[4] = {sv.x, sv.y, sv.z, sv.w};
 #pragma unroll
-        for (int a = 0; a < 4; ++a)
-            if (r0 + 32 * a < rows) q[a] = __ldcs(reinterpret_cast<const uint32_t*>(codes + (r0 + 32 * a) * (d / 2) + c / 2));
+        for (int a = 0; a < 4; ++a) {
+            q[a] = make_uint2(0, 0);
+            if (r0 + 32 * a < rows)
+                q[a] = __ldg(reinterpret_cast<const uint2*>(codes + (r0 + 32 * a) * (d >> 1) + (c >> 1)));
+        }
 #pragma unroll
         for (int a = 0; a < 4; ++a) {
             const int64_t row = r0 + 32 * a;
             if (row >= rows) break;
-            const uint32_t byte = (sw[a] >> (8 * ((c / BLOCK) & 3))) & 0xff;
+            const uint32_t byte = sw[a] >> (8 * (c / BLOCK & 3)) & 0xff;
             float s;
             if (BLOCK == 32)
-                s = byte == 0xff ? __uint_as_float(0x7fffffffu) : pow2_byte(byte);
+                s = byte == 0xff ? NAN : pow2_byte(byte);
             else
-                s = byte == 0x7f ? __uint_as_float(0x7fffffffu) : from_e4m3(byte & 0x7f);
-            const float gr = g ? __ldg(g + row / rows_per_g) : 1.f;
-            float v[8];
+                s = byte == 0x7f ? NAN : from_e4m3(byte & 0x7f);
+            const float gr = SCALED ? __ldg(g + row / rows_per_g) : 1.f;
+            float v[16];
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                // e2m1: eem -> the number with exponent and mantissa bits in place, scaled by 2^126
-                const uint32_t code = q[a] >> (4 * i);
-                const uint32_t mag = code & 7;
-                const float m = mag < 2 ? 0.5f * (float)mag : __uint_as_float(((mag >> 1) + 126) << 23 | (mag & 1) << 22);
-                v[i] = __uint_as_float(__float_as_uint(m) | (code & 8) << 28) * s;
+            for (int h = 0; h < 2; ++h) {
+                __half2 m[4];
+                from_e2m1x8(h ? q[a].y : q[a].x, m);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const float2 f = __half22float2(m[i]);
+                    v[8 * h + 2 * i] = f.x * s;
+                    v[8 * h + 2 * i + 1] = f.y * s;
+                }
             }
+            uint32_t o[8];
             if (F32) {
-                float4* o = reinterpret_cast<float4*>(reinterpret_cast<float*>(out) + row * d + c);
-                __stcs(o, make_float4(v[0] * gr, v[1] * gr, v[2] * gr, v[3] * gr));
-                __stcs(o + 1, make_float4(v[4] * gr, v[5] * gr, v[6] * gr, v[7] * gr));
-            } else {
-                uint32_t o[4];
+                float* y = reinterpret_cast<float*>(out) + row * d + c;
 #pragma unroll
-                for (int i = 0; i < 4; ++i) o[i] = bf16_once(v[2 * i], gr) | bf16_once(v[2 * i + 1], gr) << 16;
-                __stcs(reinterpret_cast<uint4*>(reinterpret_cast<__nv_bfloat16*>(out) + row * d + c),
-                       make_uint4(o[0], o[1], o[2], o[3]));
+                for (int h = 0; h < 2; ++h) {
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) o[i] = __float_as_uint(SCALED ? v[8 * h + i] * gr : v[8 * h + i]);
+                    store32(y + 8 * h, wide, o);
+                }
+            } else {
+#pragma unroll
+                for (int i = 0; i < 8; ++i)
+                    o[i] = SCALED ? pack_bf16(sticky(v[2 * i], gr), sticky(v[2 * i + 1], gr))
+                                  : pack_bf16(v[2 * i], v[2 * i + 1]);
+                store32(reinterpret_cast<__nv_bfloat16*>(out) + row * d + c, wide, o);
             }
         }
     }
@@ -313,14 +399,14 @@ __global__ void __launch_bounds__(kThreads) fp4_dequantize_kernel(const uint8_t*
 // ------------------------------------------------------------------------------ matrix scale
 // max|x| as bits (ordered like the magnitudes; NaN above infinity), one atomic a block: order-free.
 template <typename T>
-__global__ void __launch_bounds__(kThreads) fp4_amax_kernel(const T* __restrict__ X, int64_t per, uint32_t* __restrict__ top) {
+__global__ void __launch_bounds__(kThreads) fp4_amax_kernel(const T* __restrict__ X, int64_t per, int wide, uint32_t* __restrict__ top) {
     const T* x = X + (int64_t)blockIdx.y * per;
     uint32_t m = 0;
-    for (int64_t i = ((int64_t)blockIdx.x * kThreads + threadIdx.x) * 8; i < per; i += (int64_t)gridDim.x * kThreads * 8) {
-        float v[8];
-        load8<T>(x + i, v);
+    for (int64_t i = ((int64_t)blockIdx.x * kThreads + threadIdx.x) * 16; i < per; i += (int64_t)gridDim.x * kThreads * 16) {
+        Raw<T> v;
+        v.load(x + i, wide);
 #pragma unroll
-        for (int j = 0; j < 8; ++j) m = max(m, __float_as_uint(v[j]) & 0x7fffffffu);
+        for (int j = 0; j < 16; ++j) m = max(m, __float_as_uint(v.at(j)) & 0x7fffffffu);
     }
     m = __reduce_max_sync(0xffffffffu, m);
     if ((threadIdx.x & 31) == 0 && m) atomicMax(top + blockIdx.y, m);
@@ -340,25 +426,25 @@ __global__ void fp4_finish_scale_kernel(uint32_t* top, int batch, float largest,
 cudaError_t launch_fp4_quantize(cudaStream_t s, int num_sms, const void* X, int x_f32, int64_t n, int d,
                                 const int32_t* perm, int64_t rows, const int64_t* seg, int E, int block, const float* g,
                                 int64_t rows_per_g, uint8_t* codes, uint8_t* scales, int* err) {
-    QuantArgs p{X, n, rows, d, perm, seg, E, g, rows_per_g, codes, scales, 0, (d + 255) / 256, err};
-    p.items = (rows + 127) / 128 * 32 * p.chunks;
+    const QuantArgs p{X, n, rows, d, perm, seg, E, g, rows_per_g, codes, scales, ((uintptr_t)X & 31) == 0, err};
     if (x_f32) return block == 32 ? launch_q<float, 32>(s, num_sms, p) : launch_q<float, 16>(s, num_sms, p);
     return block == 32 ? launch_q<__nv_bfloat16, 32>(s, num_sms, p) : launch_q<__nv_bfloat16, 16>(s, num_sms, p);
 }
 
 cudaError_t launch_fp4_dequantize(cudaStream_t s, int num_sms, const uint8_t* codes, const uint8_t* scales, int64_t rows,
                                   int d, int block, const float* g, int64_t rows_per_g, void* out, int out_f32) {
-    const int chunks = (d + 255) / 256;
-    const int64_t items = (rows + 127) / 128 * 32 * chunks;
-    int64_t blocks = (items + kThreads / 32 - 1) / (kThreads / 32);
-    if (blocks > (int64_t)num_sms * 32) blocks = (int64_t)num_sms * 32;
-#define CLHA_DQ(B, F) \
-    fp4_dequantize_kernel<B, F><<<(unsigned)blocks, kThreads, 0, s>>>(codes, scales, rows, d, g, rows_per_g, items, chunks, out)
+    const unsigned blocks = item_blocks((rows + 127) / 128 * 32 * (d >> 7), num_sms);
+    const int wide = ((uintptr_t)out & 31) == 0;
+#define CLHA_DQ(B, F, S) \
+    fp4_dequantize_kernel<B, F, S><<<blocks, kThreads, 0, s>>>(codes, scales, rows, d, g, rows_per_g, wide, out)
+#define CLHA_DQ2(B, F) \
+    if (g) CLHA_DQ(B, F, true); else CLHA_DQ(B, F, false)
     if (block == 32) {
-        if (out_f32) CLHA_DQ(32, true); else CLHA_DQ(32, false);
+        if (out_f32) { CLHA_DQ2(32, true); } else { CLHA_DQ2(32, false); }
     } else {
-        if (out_f32) CLHA_DQ(16, true); else CLHA_DQ(16, false);
+        if (out_f32) { CLHA_DQ2(16, true); } else { CLHA_DQ2(16, false); }
     }
+#undef CLHA_DQ2
 #undef CLHA_DQ
     clha_note_launches(1);
     return cudaGetLastError();
@@ -369,14 +455,15 @@ cudaError_t launch_fp4_tensor_scale(cudaStream_t s, int num_sms, const void* X, 
     cudaError_t e = cudaMemsetAsync(scale, 0, (size_t)batch * sizeof(float), s);
     if (e != cudaSuccess) return e;
     if (per) {
-        int64_t blocks = (per + kThreads * 8 * 4 - 1) / (kThreads * 8 * 4);
+        int64_t blocks = (per + kThreads * 16 * 2 - 1) / (kThreads * 16 * 2);
         const int64_t most = ((int64_t)num_sms * 8 + batch - 1) / batch;
         if (blocks > most) blocks = most;
         const dim3 grid((unsigned)blocks, (unsigned)batch);
+        const int wide = ((uintptr_t)X & 31) == 0;             // (every matrix then is: per is a multiple of 128)
         if (x_f32)
-            fp4_amax_kernel<float><<<grid, kThreads, 0, s>>>((const float*)X, per, (uint32_t*)scale);
+            fp4_amax_kernel<float><<<grid, kThreads, 0, s>>>((const float*)X, per, wide, (uint32_t*)scale);
         else
-            fp4_amax_kernel<__nv_bfloat16><<<grid, kThreads, 0, s>>>((const __nv_bfloat16*)X, per, (uint32_t*)scale);
+            fp4_amax_kernel<__nv_bfloat16><<<grid, kThreads, 0, s>>>((const __nv_bfloat16*)X, per, wide, (uint32_t*)scale);
         clha_note_launches(1);
     }
     // the largest value of the format: 6 times the largest scale that a block of it may take
