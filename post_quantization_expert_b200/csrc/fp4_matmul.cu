@@ -2,44 +2,53 @@
 // h = SiLU(X Wg^T) * (X Wu^T), dense or over routed segments.
 //
 // tcgen05.mma multiplies e2m1 values and applies both operands' block scales, accumulating in float32;
-// the matrix scales multiply the finished sums in the epilogue. One CTA computes 128 rows of X by NB
-// blocks of 128 rows of W (for the gate/up pair one block of each, so that SiLU(g) * u needs nothing from
-// outside the tile):
-//   warp 0     TMA producer: per 256 columns of K, 128 bytes a row of X and of W (128-byte swizzle) and
-//              their scale tiles (512 bytes for 128 rows x 4 blocks, copied as they lie).
-//   warp 1     copies the stage's scale tiles to TMEM (its own columns for each stage, so that the stage's
-//              barrier also orders their reuse) and issues the products of 64 columns of K each.
-//   warps 2-9  epilogue: two warps for each TMEM lane quadrant.
-// Segments start at multiples of 128, so a tile never mixes experts. Rows of a segment behind its tokens
-// are written as zero; rows behind the last segment are not touched.
+// the matrix scales multiply the finished sums in the epilogue. Two kernels, by the number of tiles: pairs of
+// SMs on large tiles (further down) where there are tiles for all of them, else the one for few rows, which
+// is bound by reading W. Segments start at multiples of 128, so a tile never mixes experts. Rows of a segment
+// behind its tokens are written as zero; rows behind the last segment are not touched.
 //
-// Few tiles (decoding) are bound by reading W: then `split` CTAs of a cluster share one tile's K range,
-// and add their parts through distributed shared memory, in rank order, so that the result does not
-// depend on timing.
+// Few rows. The tensor core's 128-row operand is W (for gate and up a block of each), its other operand the
+// tile's rows of X, as many as hold tokens, in steps of 16: a decoding step pays for 16 rows, not for 128,
+// and more of shared memory is left for W's copies in flight.
+//   warp 0       TMA producer: per 256 columns of K, 128 bytes a row of W and of X (128-byte swizzle) and
+//                their scale tiles (512 bytes for 128 rows x 4 blocks, copied as they lie).
+//   warp 1       issues the products of 64 columns of K each.
+//   warps 2-9    epilogue: two warps for each TMEM lane quadrant (32 columns of Y), rows in turns.
+//   warps 10, 11 copy the stage's scale tiles to TMEM, every other one each (its own TMEM columns for each
+//                stage, so that the stage's barriers also order their reuse).
+// With few tiles, `split` CTAs of a cluster share one tile's K range and add their parts through distributed
+// shared memory, in rank order, so that the result does not depend on timing.
 #include "clha_internal.h"
 #include "tc_ptx.h"
 #include "tmap.h"
 
 namespace {
 
-constexpr int kThreads = 320;
-constexpr int BM = 128, BKB = 128;              // rows of X; bytes of K a stage (256 columns)
-constexpr int TILE_BYTES = 128 * BKB;           // 16 KB: one operand block of a stage
+constexpr int kThreads = 384;
+constexpr int BKB = 128;                        // bytes of K a stage (256 columns)
+constexpr int TILE_BYTES = 128 * BKB;           // 16 KB: 128 rows of a stage
 constexpr int MAX_SMEM = 232448;
+constexpr int kMaxE = 1024;
 
-template <int BLOCK, int NB>
+// NB blocks of W (2: gate and up), at most XR rows of X a tile
+template <int BLOCK, int NB, int XR>
 struct Cfg {
-    static constexpr int APS = 256 / BLOCK / 4;              // scale tiles of 512 bytes a stage and operand block
+    static constexpr int APS = 256 / BLOCK / 4;              // scale tiles of 512 bytes a stage and 128 rows
     static constexpr int SF_BYTES = APS * 512;
-    static constexpr int STAGE_BYTES = (1 + NB) * (TILE_BYTES + SF_BYTES);
-    static constexpr int STAGES = NB == 1 ? 6 : 4;
-    static constexpr int ACCS = NB == 1 ? 2 : 1;             // accumulators of NB * 128 columns: 256 in all
+    static constexpr int STAGE_BYTES = NB * TILE_BYTES + XR * BKB + (NB + 1) * SF_BYTES;
+    static constexpr int ACCS = NB == 1 || XR < 128 ? 2 : 1; // accumulators of NB * XR columns
     static constexpr int SF_COLS = APS * 4 * (1 + NB);       // TMEM columns of a stage's scales
-    static constexpr int BAR_OFF = STAGES * STAGE_BYTES;
-    static constexpr int SMEM = BAR_OFF + 8 * (2 * STAGES + 2 * ACCS + 1) + 16 + 1024;
-    static_assert(SMEM <= MAX_SMEM, "shared memory");
-    static_assert(256 + STAGES * SF_COLS <= 512, "tensor memory");
-    static_assert(STAGES * STAGE_BYTES >= 128 * NB * 128 * 4, "partial sums fit the stages");
+    static constexpr int SF_BASE = ACCS * NB * XR;
+    static constexpr int SEG_BYTES = (2 * kMaxE + 2) * 4;
+    static constexpr int FIT = (MAX_SMEM - 1024 - SEG_BYTES - 512) / STAGE_BYTES;
+    static constexpr int TFIT = (512 - SF_BASE) / SF_COLS;
+    static constexpr int STAGES = FIT < TFIT ? FIT : TFIT;
+    static constexpr int SEG_OFF = STAGES * STAGE_BYTES;
+    static constexpr int BAR_OFF = SEG_OFF + SEG_BYTES;
+    static constexpr int SMEM = BAR_OFF + 8 * (3 * STAGES + 2 * ACCS + 1) + 16 + 1024;
+    static_assert(SMEM <= MAX_SMEM && STAGES >= 4, "shared memory");
+    static_assert(STAGE_BYTES % 1024 == 0 && BAR_OFF % 8 == 0, "alignment");
+    static_assert(STAGES * STAGE_BYTES >= NB * XR * 128 * 4, "partial sums fit the stages");
 };
 
 struct MatmulArgs {
@@ -55,33 +64,6 @@ struct MatmulArgs {
     int split;               // CTAs of a cluster that share a tile's K
     int* err;
 };
-
-__device__ __forceinline__ int find_segment(const int64_t* seg, int E, int64_t row) {
-    int lo = 0, hi = E - 1;
-    while (lo < hi) {  // last e with seg[e] <= row
-        int mid = (lo + hi + 1) >> 1;
-        if (seg[mid] <= row) lo = mid; else hi = mid - 1;
-    }
-    return lo;
-}
-
-struct Tile {
-    int64_t m0, vend;        // first row; end of the rows with a token
-    int n0, e;
-};
-
-__device__ __forceinline__ Tile decode(const MatmulArgs& p, int64_t w, int tile_n) {
-    Tile t;
-    t.m0 = w / p.n_tiles * BM;
-    t.n0 = (int)(w % p.n_tiles) * tile_n;
-    t.e = 0;
-    t.vend = p.rows;
-    if (p.seg) {
-        t.e = find_segment(p.seg, p.E, t.m0);
-        t.vend = p.seg[t.e] + p.seg[p.E + 1 + t.e];
-    }
-    return t;
-}
 
 __device__ __forceinline__ float silu_mul(float g, float u) { return __fdividef(g, 1.f + __expf(-g)) * u; }
 
@@ -100,6 +82,8 @@ template <>
 __device__ __forceinline__ void store4<__nv_bfloat16>(__nv_bfloat16* y, float a, float b, float c, float d) {
     *reinterpret_cast<uint2*>(y) = make_uint2(pack_bf16(a, b), pack_bf16(c, d));
 }
+__device__ __forceinline__ void store1(float* y, float v) { *y = v; }
+__device__ __forceinline__ void store1(__nv_bfloat16* y, float v) { *y = __float2bfloat16_rn(v); }
 __device__ __forceinline__ float4 ld_cluster_f4(uint32_t addr) {
     float4 v;
     asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
@@ -107,30 +91,31 @@ __device__ __forceinline__ float4 ld_cluster_f4(uint32_t addr) {
     return v;
 }
 
-// byte of element (row, 4-column group c4) in the partial sums' [128][NB * 128] float32 array; groups of a
-// row are permuted by the row so that eight rows' same group fall into different banks
-template <int NB>
-__device__ __forceinline__ uint32_t part_off(int row, int c4) {
-    return (uint32_t)(row * (NB * 512) + ((c4 ^ (row & 7)) << 4));
-}
+// ------------------------------------------------------------------------------ few rows
+struct Tile {
+    int64_t m0;              // first row
+    int n0, e;               // first column; expert
+    int tokens, height;      // rows with a token; rows that are written
+};
 
-template <int BLOCK, int NB, bool ACT, typename OUT>
+template <int BLOCK, int NB, int XR, typename OUT>
 __global__ void __launch_bounds__(kThreads, 1)
 fp4_matmul_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ CUtensorMap tmXs,
                   const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUtensorMap tmWs,
                   const __grid_constant__ CUtensorMap tmU, const __grid_constant__ CUtensorMap tmUs, MatmulArgs p) {
-    static_assert(!ACT || NB == 2, "gate and up blocks");
-    using C = Cfg<BLOCK, NB>;
-    constexpr int TILE_N = ACT ? 128 : NB * 128;
+    using C = Cfg<BLOCK, NB, XR>;
+    constexpr bool ACT = NB == 2;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    int* seg = reinterpret_cast<int*>(smem + C::SEG_OFF);          // starts [E + 1], then token counts [E]
     uint64_t* bars = reinterpret_cast<uint64_t*>(smem + C::BAR_OFF);
     const uint32_t full0 = tc::smem_u32(bars);
     const uint32_t empty0 = full0 + 8 * C::STAGES;
-    const uint32_t tfull0 = empty0 + 8 * C::STAGES;       // accumulator a holds a finished tile
+    const uint32_t sready0 = empty0 + 8 * C::STAGES;      // a stage's scales are on their way to TMEM
+    const uint32_t tfull0 = sready0 + 8 * C::STAGES;      // accumulator a holds a finished tile
     const uint32_t tempty0 = tfull0 + 8 * C::ACCS;        // accumulator a has been read
     const uint32_t drain = tempty0 + 8 * C::ACCS;
-    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 2 * C::STAGES + 2 * C::ACCS + 1);
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 3 * C::STAGES + 2 * C::ACCS + 1);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int S = p.split;
@@ -140,57 +125,78 @@ fp4_matmul_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant
         for (int s = 0; s < C::STAGES; ++s) {
             tc::mbar_init(full0 + 8 * s, 1);
             tc::mbar_init(empty0 + 8 * s, 1);
+            tc::mbar_init(sready0 + 8 * s, 2);            // one arrival per scale warp
         }
         for (int a = 0; a < C::ACCS; ++a) {
             tc::mbar_init(tfull0 + 8 * a, 1);
             tc::mbar_init(tempty0 + 8 * a, 8);            // one arrival per epilogue warp
         }
-        tc::mbar_init(drain, 1);
+        tc::mbar_init(drain, 3);                          // the products' thread and the scale warps
         *abort_flag = 0;
         tc::fence_barrier_init();
+        tc::prefetch_tmap(&tmX);
+        tc::prefetch_tmap(&tmXs);
+        tc::prefetch_tmap(&tmW);
+        tc::prefetch_tmap(&tmWs);
     }
+    if (p.seg)
+        for (int i = threadIdx.x; i <= 2 * p.E; i += kThreads) seg[i] = (int)p.seg[i];
     if (warp == 1) tc::tmem_alloc(tc::smem_u32(tmem_slot), 512);
     tc::fence_before_sync();
     __syncthreads();
     tc::fence_after_sync();
     const uint32_t tmem = *tmem_slot;
 
-    const int64_t used = p.seg ? p.seg[p.E] : p.rows;
-    const int64_t total = (used + BM - 1) / BM * p.n_tiles;
+    const int64_t used = p.seg ? min((int64_t)seg[p.E], p.rows) : p.rows;
+    const int64_t total = (used + XR - 1) / XR * p.n_tiles;        // (segments are tiled by 128 rows: XR = 128 then)
     const int64_t w0 = S > 1 ? blockIdx.x / S : blockIdx.x, stride = S > 1 ? gridDim.x / S : gridDim.x;
     const int nk = (p.K + 255) / 256;
     const int atoms = p.K / BLOCK / 4;                     // scale tiles across a row tile
     const int k_lo = (int)((int64_t)nk * rank / S), k_hi = (int)((int64_t)nk * (rank + 1) / S);
     // split > 1 runs one tile a cluster (the grid covers them all): the stages then hold the partial sums
 
+    const auto tile = [&](int64_t w) {
+        Tile t;
+        t.m0 = w / p.n_tiles * XR;
+        t.n0 = (int)(w % p.n_tiles) * 128;
+        t.height = (int)min((int64_t)XR, used - t.m0);
+        t.e = 0;
+        t.tokens = t.height;
+        if (p.seg) {
+            int lo = 0, hi = p.E - 1;
+            while (lo < hi) {                              // last e with seg[e] <= m0
+                const int mid = (lo + hi + 1) >> 1;
+                if (seg[mid] <= t.m0) lo = mid; else hi = mid - 1;
+            }
+            t.e = lo;
+            t.tokens = max(0, min(t.height, seg[lo] + seg[p.E + 1 + lo] - (int)t.m0));
+        }
+        return t;
+    };
+
     if (warp == 0) {
         if (lane == 0) {
-            tc::prefetch_tmap(&tmX);
-            tc::prefetch_tmap(&tmXs);
-            tc::prefetch_tmap(&tmW);
-            tc::prefetch_tmap(&tmWs);
             int it = 0;
             bool ok = true;
             for (int64_t w = w0; ok && w < total; w += stride) {
-                const Tile t = decode(p, w, TILE_N);
+                const Tile t = tile(w);
+                const int boxes = (t.tokens + 15) / 16;
                 const int wr = t.e * p.N + t.n0;
                 for (int kb = k_lo; kb < k_hi; ++kb, ++it) {
                     const int s = it % C::STAGES;
                     if (!tc::mbar_wait_bounded(empty0 + 8 * s, ((it / C::STAGES) & 1) ^ 1, abort_flag)) { ok = false; break; }
                     const uint32_t fb = full0 + 8 * s;
-                    tc::mbar_arrive_expect_tx(fb, C::STAGE_BYTES);
+                    tc::mbar_arrive_expect_tx(fb, NB * TILE_BYTES + boxes * 16 * BKB + (NB + 1) * C::SF_BYTES);
                     const uint32_t a = tc::smem_u32(smem + s * C::STAGE_BYTES);
-                    const uint32_t b = a + TILE_BYTES;
-                    const uint32_t sf = b + NB * TILE_BYTES;
-                    tc::tma_load_2d(a, &tmX, fb, kb * BKB, (int)t.m0);
-                    tc::tma_load_2d(sf, &tmXs, fb, 0, (int)(t.m0 / 128) * atoms + kb * C::APS);
-                    tc::tma_load_2d(b, &tmW, fb, kb * BKB, wr);
-                    tc::tma_load_2d(sf + C::SF_BYTES, &tmWs, fb, 0, wr / 128 * atoms + kb * C::APS);
-                    if (NB == 2) {   // the up projection's block, or the next 128 columns
-                        const int ur = ACT ? wr : wr + 128;
-                        tc::tma_load_2d(b + TILE_BYTES, ACT ? &tmU : &tmW, fb, kb * BKB, ur);
-                        tc::tma_load_2d(sf + 2 * C::SF_BYTES, ACT ? &tmUs : &tmWs, fb, 0, ur / 128 * atoms + kb * C::APS);
+                    const uint32_t b = a + NB * TILE_BYTES, sf = b + XR * BKB;
+                    tc::tma_load_2d(a, &tmW, fb, kb * BKB, wr);
+                    tc::tma_load_2d(sf, &tmWs, fb, 0, wr / 128 * atoms + kb * C::APS);
+                    if (ACT) {
+                        tc::tma_load_2d(a + TILE_BYTES, &tmU, fb, kb * BKB, wr);
+                        tc::tma_load_2d(sf + C::SF_BYTES, &tmUs, fb, 0, wr / 128 * atoms + kb * C::APS);
                     }
+                    tc::tma_load_2d(sf + NB * C::SF_BYTES, &tmXs, fb, 0, (int)(t.m0 / 128) * atoms + kb * C::APS);
+                    for (int x = 0; x < boxes; ++x) tc::tma_load_2d(b + x * 16 * BKB, &tmX, fb, kb * BKB, (int)t.m0 + 16 * x);
                 }
             }
             if (!ok) {  // the copies already issued land before the CTA exits
@@ -201,38 +207,37 @@ fp4_matmul_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant
         __syncwarp();
     } else if (warp == 1) {
         if (lane == 0) {
-            constexpr uint32_t kE8 = BLOCK == 32;
-            constexpr uint32_t ID0 = tc::idesc_fp4(kE8, BM, NB * 128, 0), ID2 = tc::idesc_fp4(kE8, BM, NB * 128, 2);
             int it = 0, tcount = 0;
             bool ok = true;
             for (int64_t w = w0; ok && w < total; w += stride, ++tcount) {
+                const Tile t = tile(w);
+                const uint32_t n16 = max(1, (t.tokens + 15) / 16);
+                const uint32_t id0 = tc::idesc_fp4(BLOCK == 32, 128, n16 * 16, 0);
+                const uint32_t id2 = tc::idesc_fp4(BLOCK == 32, 128, n16 * 16, 2);
                 const int acc = tcount % C::ACCS;
                 if (!tc::mbar_wait_bounded(tempty0 + 8 * acc, ((tcount / C::ACCS) & 1) ^ 1, abort_flag)) { ok = false; break; }
                 tc::fence_after_sync();
-                const uint32_t d_tmem = tmem + acc * (NB * 128);
+                const uint32_t d_tmem = tmem + acc * (NB * XR);
                 for (int kb = k_lo; kb < k_hi; ++kb, ++it) {
                     const int s = it % C::STAGES;
-                    if (!tc::mbar_wait_bounded(full0 + 8 * s, (it / C::STAGES) & 1, abort_flag)) { ok = false; break; }
+                    const uint32_t ph = (it / C::STAGES) & 1;
+                    if (!tc::mbar_wait_bounded(full0 + 8 * s, ph, abort_flag) ||
+                        !tc::mbar_wait_bounded(sready0 + 8 * s, ph, abort_flag)) { ok = false; break; }
                     tc::fence_after_sync();
                     const uint32_t a = tc::smem_u32(smem + s * C::STAGE_BYTES);
-                    const uint32_t b = a + TILE_BYTES;
-                    const uint32_t sf = b + NB * TILE_BYTES;
-                    const uint32_t ta = tmem + 256 + s * C::SF_COLS, tb = ta + C::APS * 4;
-#pragma unroll
-                    for (int j = 0; j < C::APS; ++j) {
-                        tc::tmem_copy_scales(ta + 4 * j, tc::plain_desc(sf + j * 512));
-#pragma unroll
-                        for (int x = 0; x < NB; ++x)
-                            tc::tmem_copy_scales(tb + 4 * (j * NB + x), tc::plain_desc(sf + (1 + x) * C::SF_BYTES + j * 512));
-                    }
+                    const uint32_t b = a + NB * TILE_BYTES;
+                    const uint32_t tw = tmem + C::SF_BASE + s * C::SF_COLS, tx = tw + NB * C::APS * 4;
                     const int steps = p.K - kb * 256 >= 256 ? 4 : 2;   // K is a multiple of 128
 #pragma unroll
                     for (int kk = 0; kk < 4; ++kk) {
                         if (kk >= steps) break;
                         const int j = BLOCK == 16 ? kk : kk >> 1;
-                        tc::mma_fp4<BLOCK>(d_tmem, tc::sw128_desc(a + kk * 32, 16, 1024), tc::sw128_desc(b + kk * 32, 16, 1024),
-                                           BLOCK == 32 && (kk & 1) ? ID2 : ID0, ta + 4 * j, tb + 4 * NB * j,
-                                           kb != k_lo || kk != 0);
+                        const uint32_t id = BLOCK == 32 && (kk & 1) ? id2 : id0;
+                        const uint64_t xd = tc::sw128_desc(b + kk * 32, 16, 1024);
+#pragma unroll
+                        for (int x = 0; x < NB; ++x)
+                            tc::mma_fp4<BLOCK>(d_tmem + x * XR, tc::sw128_desc(a + x * TILE_BYTES + kk * 32, 16, 1024), xd, id,
+                                               tw + 4 * (x * C::APS + j), tx + 4 * j, kb != k_lo || kk != 0);
                     }
                     tc::mma_commit(empty0 + 8 * s);
                 }
@@ -240,103 +245,108 @@ fp4_matmul_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant
             }
         }
         __syncwarp();
+    } else if (warp >= 10) {
+        if (lane == 0) {
+            int it = 0;
+            bool ok = true;
+            for (int64_t w = w0; ok && w < total; w += stride)
+                for (int kb = k_lo; kb < k_hi; ++kb, ++it) {
+                    const int s = it % C::STAGES;
+                    if (!tc::mbar_wait_bounded(full0 + 8 * s, (it / C::STAGES) & 1, abort_flag)) { ok = false; break; }
+                    tc::fence_after_sync();
+                    const uint32_t sf = tc::smem_u32(smem + s * C::STAGE_BYTES) + NB * TILE_BYTES + XR * BKB;
+                    const uint32_t ts = tmem + C::SF_BASE + s * C::SF_COLS;
+#pragma unroll
+                    for (int j = 0; j < (NB + 1) * C::APS; ++j)
+                        if ((j & 1) == warp - 10) tc::tmem_copy_scales(ts + 4 * j, tc::plain_desc(sf + j * 512));
+                    tc::mma_commit(sready0 + 8 * s);
+                }
+            tc::mma_commit(drain);   // the copies that this thread issued are done before the CTA gives its TMEM back
+        }
+        __syncwarp();
     } else {
         const int q = warp & 3, half = (warp - 2) >> 2;
         const float xg = p.xg ? __ldg(p.xg) : 1.f;
         OUT* Y = reinterpret_cast<OUT*>(p.Y);
+        float* part = reinterpret_cast<float*>(smem);              // [NB][XR][128], for split > 1
         int tcount = 0;
         for (int64_t w = w0; w < total; w += stride, ++tcount) {
-            const Tile t = decode(p, w, TILE_N);
+            const Tile t = tile(w);
             const int acc = tcount % C::ACCS;
+            const float ag = xg * (p.wg ? __ldg(p.wg + t.e) : 1.f);
+            const float au = ACT ? xg * (p.ug ? __ldg(p.ug + t.e) : 1.f) : 0.f;
             if (!tc::mbar_wait_bounded(tfull0 + 8 * acc, (tcount / C::ACCS) & 1, abort_flag)) break;
             tc::fence_after_sync();
-            // this warp's columns: a half of the tile's (of both blocks' for gate and up)
-            const uint32_t tb = tmem + acc * (NB * 128) + ((uint32_t)(q * 32) << 16);
-            uint32_t v[2 * NB][32];
+            const uint32_t tb = tmem + acc * (NB * XR) + ((uint32_t)(q * 32) << 16);
+            const int col = q * 32 + lane;                         // of the tile's 128
+            for (int r0 = half * 32; r0 < t.tokens; r0 += 64) {
+                uint32_t v[NB][32];
 #pragma unroll
-            for (int i = 0; i < 2 * NB; ++i) {
-                const int col = ACT ? (i >> 1) * 128 + half * 64 + (i & 1) * 32 : half * (NB * 64) + i * 32;
-                tc::tmem_ld_32x32b_x32(tb + col, v[i]);
+                for (int x = 0; x < NB; ++x) tc::tmem_ld_32x32b_x32(tb + x * XR + r0, v[x]);
+                tc::tmem_wait_ld();
+                if (S > 1) {
+#pragma unroll
+                    for (int j = 0; j < 32; ++j)
+                        if (r0 + j < t.tokens)
+#pragma unroll
+                            for (int x = 0; x < NB; ++x)
+                                part[(x * XR + r0 + j) * 128 + col] = __uint_as_float(v[x][j]);
+                    continue;
+                }
+                OUT* y = Y + (t.m0 + r0) * p.N + t.n0 + col;
+#pragma unroll
+                for (int j = 0; j < 32; ++j)
+                    if (r0 + j < t.tokens) {
+                        const float a = __uint_as_float(v[0][j]) * ag;
+                        store1(y + (int64_t)j * p.N, ACT ? silu_mul(a, __uint_as_float(v[NB - 1][j]) * au) : a);
+                    }
             }
-            tc::tmem_wait_ld();
             tc::fence_before_sync();
             __syncwarp();
             if (lane == 0) tc::mbar_arrive(tempty0 + 8 * acc);
-            const int lr = q * 32 + lane;
-            const int64_t row = t.m0 + lr;
-            if (S > 1) {
-                const uint32_t part = tc::smem_u32(smem);
-#pragma unroll
-                for (int i = 0; i < 2 * NB; ++i) {
-                    const int col = ACT ? (i >> 1) * 128 + half * 64 + (i & 1) * 32 : half * (NB * 64) + i * 32;
-#pragma unroll
-                    for (int j = 0; j < 8; ++j)
-                        asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};"
-                                     ::"r"(part + part_off<NB>(lr, col / 4 + j)), "r"(v[i][4 * j]), "r"(v[i][4 * j + 1]),
-                                     "r"(v[i][4 * j + 2]), "r"(v[i][4 * j + 3]) : "memory");
-                }
-                continue;
-            }
-            if (row >= p.rows) continue;
-            const bool real = row < t.vend;
-            const float ag = real ? xg * (p.wg ? __ldg(p.wg + t.e) : 1.f) : 0.f;
-            const float au = ACT ? (real ? xg * (p.ug ? __ldg(p.ug + t.e) : 1.f) : 0.f) : 0.f;
-            const int col = t.n0 + half * (ACT ? 64 : NB * 64);
-            if (!ACT && NB == 2 && col >= p.N) continue;       // N is an odd number of 128-column blocks
-            OUT* y = Y + row * p.N + col;
-#pragma unroll
-            for (int i = 0; i < (ACT ? 2 : 2 * NB); ++i)
-#pragma unroll
-                for (int j = 0; j < 32; j += 4) {
-                    float o[4];
-#pragma unroll
-                    for (int x = 0; x < 4; ++x) {
-                        const float a = __uint_as_float(v[i][j + x]) * ag;
-                        o[x] = ACT ? silu_mul(a, __uint_as_float(v[ACT ? i + 2 : i][j + x]) * au) : a;
-                        if (!real) o[x] = 0.f;
-                    }
-                    store4<OUT>(y + i * 32 + j, o[0], o[1], o[2], o[3]);
-                }
+            if (S > 1) continue;
+            // rows behind the segment's tokens: zeros, 16 bytes a lane
+            constexpr int PER = 16 / (int)sizeof(OUT);
+            const int in_row = 128 / PER;
+            for (int i = (warp - 2) * 32 + lane; i < (t.height - t.tokens) * in_row; i += 256)
+                *reinterpret_cast<uint4*>(Y + (t.m0 + t.tokens + i / in_row) * p.N + t.n0 + i % in_row * PER) =
+                    make_uint4(0, 0, 0, 0);
         }
         __syncwarp();
     }
 
     if (S > 1) {
-        // every CTA's part of the tile is in its shared memory; each CTA adds a 1/S share of the columns
+        // every CTA's part of the tile is in its shared memory; each CTA adds a 1/S share of it
         __syncthreads();
         tc::cluster_sync();
         if (w0 < total && !*abort_flag) {
-            const Tile t = decode(p, w0, TILE_N);
+            const Tile t = tile(w0);
             const float xg = p.xg ? __ldg(p.xg) : 1.f;
             const float ag = xg * (p.wg ? __ldg(p.wg + t.e) : 1.f);
             const float au = ACT ? xg * (p.ug ? __ldg(p.ug + t.e) : 1.f) : 0.f;
-            const int groups = TILE_N / 4 / S;                 // 4-column groups of this CTA
-            const int64_t last = used < p.rows ? used : p.rows;
-            const int n_rows = (int)(last - t.m0 < BM ? last - t.m0 : BM);
+            const int groups = 32 / S;                             // 4-column groups of this CTA
             const uint32_t part = tc::smem_u32(smem);
             OUT* Y = reinterpret_cast<OUT*>(p.Y);
-            for (int i = threadIdx.x; i < n_rows * groups; i += kThreads) {
-                const int lr = i / groups, c4 = rank * groups + i % groups;
+            for (int i = threadIdx.x; i < t.height * groups; i += kThreads) {
+                const int r = i / groups, c4 = rank * groups + i % groups;
                 float a[4] = {}, u[4] = {};
-                const bool real = t.m0 + lr < t.vend;
-                if (real)
+                if (r < t.tokens) {
                     for (int s = 0; s < S; ++s) {
-                        const uint32_t base = tc::mapa_shared(part, s);
-                        const float4 x = ld_cluster_f4(base + part_off<NB>(lr, c4));
+                        const uint32_t base = tc::mapa_shared(part, s) + (r * 128 + c4 * 4) * 4;
+                        const float4 x = ld_cluster_f4(base);
                         a[0] += x.x; a[1] += x.y; a[2] += x.z; a[3] += x.w;
                         if (ACT) {
-                            const float4 z = ld_cluster_f4(base + part_off<NB>(lr, c4 + 32));
+                            const float4 z = ld_cluster_f4(base + XR * 512);
                             u[0] += z.x; u[1] += z.y; u[2] += z.z; u[3] += z.w;
                         }
                     }
-                if (!ACT && NB == 2 && t.n0 + c4 * 4 >= p.N) continue;
 #pragma unroll
-                for (int x = 0; x < 4; ++x)
-                    a[x] = !real ? 0.f : ACT ? silu_mul(a[x] * ag, u[x] * au) : a[x] * ag;
-                store4<OUT>(Y + (t.m0 + lr) * p.N + t.n0 + c4 * 4, a[0], a[1], a[2], a[3]);
+                    for (int x = 0; x < 4; ++x) a[x] = ACT ? silu_mul(a[x] * ag, u[x] * au) : a[x] * ag;
+                }
+                store4<OUT>(Y + (t.m0 + r) * p.N + t.n0 + c4 * 4, a[0], a[1], a[2], a[3]);
             }
         }
-        tc::cluster_sync();                                    // the others have read this CTA's part
+        tc::cluster_sync();                                        // the others have read this CTA's part
     } else {
         __syncthreads();
     }
@@ -382,7 +392,6 @@ struct PairCfg {
     static_assert(256 + STAGES * SF_COLS <= 512, "tensor memory");
 };
 constexpr int kBand = 8;
-constexpr int kPairThreads = 384;   // as above, and warps 10 and 11 for the scales
 
 // The tiles in order: expert after expert, each expert's in bands. A role asks with ascending w.
 struct Walk {
@@ -410,7 +419,7 @@ struct Walk {
 };
 
 template <int BLOCK, bool ACT, typename OUT>
-__global__ void __launch_bounds__(kPairThreads, 1)
+__global__ void __launch_bounds__(kThreads, 1)
 fp4_matmul_pair_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ CUtensorMap tmXs,
                        const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUtensorMap tmWs,
                        const __grid_constant__ CUtensorMap tmU, const __grid_constant__ CUtensorMap tmUs,
@@ -642,12 +651,12 @@ struct Maps {
 };
 
 template <int BLOCK, bool ACT>
-cudaError_t make_maps(const Fp4Product& a, int y_size, Maps& t) {
+cudaError_t make_maps(const Fp4Product& a, int y_size, int x_box, Maps& t) {
     constexpr int APS = 256 / BLOCK / 4;
     const int atoms = a.K / BLOCK / 4;
     const uint64_t x_tiles = (uint64_t)((a.rows + 127) / 128), w_rows = (uint64_t)a.E * a.N;
     cudaError_t e;
-    if ((e = make_tmap_2d(&t.X, a.xq, (uint64_t)a.rows, (uint64_t)a.K / 2, 1, 128, BKB)) != cudaSuccess) return e;
+    if ((e = make_tmap_2d(&t.X, a.xq, (uint64_t)a.rows, (uint64_t)a.K / 2, 1, x_box, BKB)) != cudaSuccess) return e;
     if ((e = make_tmap_2d_u32(&t.Xs, a.xs, x_tiles * atoms, 128, APS, 128)) != cudaSuccess) return e;
     if ((e = make_tmap_2d(&t.W, a.wq, w_rows, (uint64_t)a.K / 2, 1, 128, BKB)) != cudaSuccess) return e;
     if ((e = make_tmap_2d_u32(&t.Ws, a.ws, w_rows / 128 * atoms, 128, APS, 128)) != cudaSuccess) return e;
@@ -671,14 +680,14 @@ template <int BLOCK, bool ACT, typename OUT>
 cudaError_t launch_pair(cudaStream_t s, int num_sms, const Fp4Product& a, int* err) {
     using C = PairCfg<BLOCK>;
     Maps t;
-    cudaError_t e = make_maps<BLOCK, ACT>(a, (int)sizeof(OUT), t);
+    cudaError_t e = make_maps<BLOCK, ACT>(a, (int)sizeof(OUT), 128, t);
     if (e != cudaSuccess) return e;
     auto kernel = fp4_matmul_pair_kernel<BLOCK, ACT, OUT>;
     if ((e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM)) != cudaSuccess) return e;
     const int tile_n = ACT ? 128 : 256;
     MatmulArgs p{a.rows, a.K, a.N, a.seg, a.E, a.xg, a.wg, a.ug, a.Y, (a.N + tile_n - 1) / tile_n, 1, err};
     cudaLaunchConfig_t cfg = {};
-    cfg.blockDim = dim3(kPairThreads);
+    cfg.blockDim = dim3(kThreads);
     cfg.dynamicSmemBytes = C::SMEM;
     cfg.stream = s;
     cfg.gridDim = dim3((unsigned)(num_sms / 2 * 2));
@@ -694,19 +703,18 @@ cudaError_t launch_pair(cudaStream_t s, int num_sms, const Fp4Product& a, int* e
     return cudaGetLastError();
 }
 
-template <int BLOCK, int NB, bool ACT, typename OUT>
-cudaError_t launch_one(cudaStream_t s, int num_sms, const Fp4Product& a, int* err) {
-    using C = Cfg<BLOCK, NB>;
+template <int BLOCK, int NB, int XR, typename OUT>
+cudaError_t launch_few(cudaStream_t s, int num_sms, const Fp4Product& a, int* err) {
+    using C = Cfg<BLOCK, NB, XR>;
     Maps t;
-    cudaError_t e = make_maps<BLOCK, ACT>(a, (int)sizeof(OUT), t);
+    cudaError_t e = make_maps<BLOCK, NB == 2>(a, (int)sizeof(OUT), 16, t);
     if (e != cudaSuccess) return e;
-    auto kernel = fp4_matmul_kernel<BLOCK, NB, ACT, OUT>;
+    auto kernel = fp4_matmul_kernel<BLOCK, NB, XR, OUT>;
     // per call: the attribute belongs to the current device's context (a process may drive several)
     if ((e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM)) != cudaSuccess) return e;
-    const int tile_n = ACT ? 128 : NB * 128;
-    MatmulArgs p{a.rows, a.K, a.N, a.seg, a.E, a.xg, a.wg, a.ug, a.Y, (a.N + tile_n - 1) / tile_n, 1, err};
-    const int64_t bound = (a.rows + 127) / 128 * p.n_tiles;              // tiles, at most
-    const int64_t expect = expected_row_tiles(a, 128) * p.n_tiles;
+    MatmulArgs p{a.rows, a.K, a.N, a.seg, a.E, a.xg, a.wg, a.ug, a.Y, a.N / 128, 1, err};
+    const int64_t bound = (a.rows + XR - 1) / XR * p.n_tiles;            // tiles, at most
+    const int64_t expect = expected_row_tiles(a, XR) * p.n_tiles;
     const int nk = (a.K + 255) / 256;
     while (p.split < 8 && expect * p.split * 2 <= num_sms && nk >= 4 * p.split) p.split *= 2;
     cudaLaunchConfig_t cfg = {};
@@ -721,23 +729,30 @@ cudaError_t launch_one(cudaStream_t s, int num_sms, const Fp4Product& a, int* er
     cfg.attrs = attr;
     cfg.numAttrs = 1;
     cfg.gridDim = dim3((unsigned)(p.split > 1 ? bound * p.split : (bound < num_sms ? bound : num_sms)));
-    e = cudaLaunchKernelEx(&cfg, kernel, t.X, t.Xs, t.W, t.Ws, t.U, t.Us, p);
-    if (e != cudaSuccess) return e;
+    if ((e = cudaLaunchKernelEx(&cfg, kernel, t.X, t.Xs, t.W, t.Ws, t.U, t.Us, p)) != cudaSuccess) return e;
     clha_note_launches(1);
     return cudaGetLastError();
+}
+
+template <int BLOCK, int NB, typename OUT>
+cudaError_t launch_product(cudaStream_t s, int num_sms, const Fp4Product& a, int* err) {
+    constexpr bool ACT = NB == 2;
+    const int tile_n = ACT ? 128 : 256;
+    if (expected_row_tiles(a, 256) * ((a.N + tile_n - 1) / tile_n) >= num_sms / 2)
+        return launch_pair<BLOCK, ACT, OUT>(s, num_sms, a, err);
+    // up to 32 dense rows: room for W's copies instead of 128 rows of X
+    if (!a.seg && a.rows <= 32) return launch_few<BLOCK, NB, 32, OUT>(s, num_sms, a, err);
+    return launch_few<BLOCK, NB, 128, OUT>(s, num_sms, a, err);
 }
 
 }  // namespace
 
 cudaError_t launch_fp4_matmul(cudaStream_t s, int num_sms, const Fp4Product& a, int block, int y_f32, int* err) {
     typedef __nv_bfloat16 bf;
-    const int tile_n = a.uq ? 128 : 256;
-    const bool pair = expected_row_tiles(a, 256) * ((a.N + tile_n - 1) / tile_n) >= num_sms / 2;
-#define CLHA_PRODUCT(B)                                                                                              \
-    (a.uq ? (pair ? launch_pair<B, true, bf>(s, num_sms, a, err) : launch_one<B, 2, true, bf>(s, num_sms, a, err))    \
-     : y_f32 ? (pair ? launch_pair<B, false, float>(s, num_sms, a, err)                                               \
-                     : launch_one<B, 1, false, float>(s, num_sms, a, err))                                            \
-             : (pair ? launch_pair<B, false, bf>(s, num_sms, a, err) : launch_one<B, 1, false, bf>(s, num_sms, a, err)))
-    return block == 32 ? CLHA_PRODUCT(32) : CLHA_PRODUCT(16);
-#undef CLHA_PRODUCT
+    if (a.uq)
+        return block == 32 ? launch_product<32, 2, bf>(s, num_sms, a, err) : launch_product<16, 2, bf>(s, num_sms, a, err);
+    if (y_f32)
+        return block == 32 ? launch_product<32, 1, float>(s, num_sms, a, err)
+                           : launch_product<16, 1, float>(s, num_sms, a, err);
+    return block == 32 ? launch_product<32, 1, bf>(s, num_sms, a, err) : launch_product<16, 1, bf>(s, num_sms, a, err);
 }
