@@ -669,10 +669,14 @@ cudaError_t make_maps(const Fp4Product& a, int y_size, int x_box, Maps& t) {
     return make_tmap_2d(&t.Y, a.Y, (uint64_t)a.rows, (uint64_t)a.N, y_size, 32, 128 / y_size);
 }
 
-// Row tiles of `height` rows to expect: segments hold rows - 128 E token slots at most (clha_packed_rows).
+// Token slots in segments of `rows` packed rows, at most (clha_packed_rows).
+int64_t slots_of(const Fp4Product& a) {
+    return a.rows - 128 * (int64_t)a.E > 0 ? a.rows - 128 * (int64_t)a.E : a.rows;
+}
+// Row tiles of `height` rows to expect.
 int64_t expected_row_tiles(const Fp4Product& a, int height) {
     if (!a.seg) return (a.rows + height - 1) / height;
-    const int64_t slots = a.rows - 128 * (int64_t)a.E > 0 ? a.rows - 128 * (int64_t)a.E : a.rows;
+    const int64_t slots = slots_of(a);
     return slots / height + (slots < a.E ? slots : a.E);
 }
 
@@ -738,7 +742,9 @@ template <int BLOCK, int NB, typename OUT>
 cudaError_t launch_product(cudaStream_t s, int num_sms, const Fp4Product& a, int* err) {
     constexpr bool ACT = NB == 2;
     const int tile_n = ACT ? 128 : 256;
-    if (expected_row_tiles(a, 256) * ((a.N + tile_n - 1) / tile_n) >= num_sms / 2)
+    // pairs where there is a tile for each and its 256 rows are not mostly empty
+    const bool full = a.seg ? slots_of(a) >= 128 * (int64_t)a.E : a.rows > 128;
+    if (full && expected_row_tiles(a, 256) * ((a.N + tile_n - 1) / tile_n) >= num_sms / 2)
         return launch_pair<BLOCK, ACT, OUT>(s, num_sms, a, err);
     // up to 32 dense rows: room for W's copies instead of 128 rows of X
     if (!a.seg && a.rows <= 32) return launch_few<BLOCK, NB, 32, OUT>(s, num_sms, a, err);
