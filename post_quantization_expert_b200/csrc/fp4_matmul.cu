@@ -39,14 +39,16 @@ struct Cfg {
     static constexpr int ACCS = NB == 1 || XR < 128 ? 2 : 1; // accumulators of NB * XR columns
     static constexpr int SF_COLS = APS * 4 * (1 + NB);       // TMEM columns of a stage's scales
     static constexpr int SF_BASE = ACCS * NB * XR;
-    static constexpr int SEG_BYTES = (2 * kMaxE + 2) * 4;
-    static constexpr int FIT = (MAX_SMEM - 1024 - SEG_BYTES - 512) / STAGE_BYTES;
-    static constexpr int TFIT = (512 - SF_BASE) / SF_COLS;
+    static constexpr int SEG_BYTES = XR < 128 ? 0 : (2 * kMaxE + 2) * 4;   // (fewer than 128 rows: dense)
+    static constexpr int CTAS = NB == 1 && XR < 128 ? 2 : 1; // of an SM
+    static constexpr int TCOLS = 512 / CTAS;                 // TMEM columns of a CTA
+    static constexpr int FIT = (MAX_SMEM / CTAS - 1024 * CTAS - SEG_BYTES - 512) / STAGE_BYTES;
+    static constexpr int TFIT = (TCOLS - SF_BASE) / SF_COLS;
     static constexpr int STAGES = FIT < TFIT ? FIT : TFIT;
     static constexpr int SEG_OFF = STAGES * STAGE_BYTES;
     static constexpr int BAR_OFF = SEG_OFF + SEG_BYTES;
     static constexpr int SMEM = BAR_OFF + 8 * (3 * STAGES + 2 * ACCS + 1) + 16 + 1024;
-    static_assert(SMEM <= MAX_SMEM && STAGES >= 4, "shared memory");
+    static_assert((SMEM + 1024) * CTAS <= MAX_SMEM + 1024 && STAGES >= 4, "shared memory");
     static_assert(STAGE_BYTES % 1024 == 0 && BAR_OFF % 8 == 0, "alignment");
     static_assert(STAGES * STAGE_BYTES >= NB * XR * 128 * 4, "partial sums fit the stages");
 };
@@ -99,7 +101,7 @@ struct Tile {
 };
 
 template <int BLOCK, int NB, int XR, typename OUT>
-__global__ void __launch_bounds__(kThreads, 1)
+__global__ void __launch_bounds__(kThreads, Cfg<BLOCK, NB, XR>::CTAS)
 fp4_matmul_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ CUtensorMap tmXs,
                   const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUtensorMap tmWs,
                   const __grid_constant__ CUtensorMap tmU, const __grid_constant__ CUtensorMap tmUs, MatmulArgs p) {
@@ -141,7 +143,7 @@ fp4_matmul_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant
     }
     if (p.seg)
         for (int i = threadIdx.x; i <= 2 * p.E; i += kThreads) seg[i] = (int)p.seg[i];
-    if (warp == 1) tc::tmem_alloc(tc::smem_u32(tmem_slot), 512);
+    if (warp == 1) tc::tmem_alloc(tc::smem_u32(tmem_slot), C::TCOLS);
     tc::fence_before_sync();
     __syncthreads();
     tc::fence_after_sync();
@@ -357,7 +359,7 @@ fp4_matmul_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant
         }
         __syncwarp();
         tc::fence_after_sync();
-        tc::tmem_dealloc(tmem, 512);
+        tc::tmem_dealloc(tmem, C::TCOLS);
     }
     if (threadIdx.x == 0 && *abort_flag) clha_record_error(p.err, CLHA_ERR_TIMEOUT, blockIdx.x, 0, KID_FP4_MATMUL);
 }
@@ -720,7 +722,8 @@ cudaError_t launch_few(cudaStream_t s, int num_sms, const Fp4Product& a, int* er
     const int64_t bound = (a.rows + XR - 1) / XR * p.n_tiles;            // tiles, at most
     const int64_t expect = expected_row_tiles(a, XR) * p.n_tiles;
     const int nk = (a.K + 255) / 256;
-    while (p.split < 8 && expect * p.split * 2 <= num_sms && nk >= 4 * p.split) p.split *= 2;
+    const int slots = num_sms * C::CTAS;
+    while (p.split < 8 && expect * p.split * 2 <= slots && nk >= 4 * p.split) p.split *= 2;
     cudaLaunchConfig_t cfg = {};
     cfg.blockDim = dim3(kThreads);
     cfg.dynamicSmemBytes = C::SMEM;
@@ -732,7 +735,7 @@ cudaError_t launch_few(cudaStream_t s, int num_sms, const Fp4Product& a, int* er
     attr[0].val.clusterDim.z = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    cfg.gridDim = dim3((unsigned)(p.split > 1 ? bound * p.split : (bound < num_sms ? bound : num_sms)));
+    cfg.gridDim = dim3((unsigned)(p.split > 1 ? bound * p.split : (bound < slots ? bound : slots)));
     if ((e = cudaLaunchKernelEx(&cfg, kernel, t.X, t.Xs, t.W, t.Ws, t.U, t.Us, p)) != cudaSuccess) return e;
     clha_note_launches(1);
     return cudaGetLastError();
