@@ -55,7 +55,35 @@ __device__ __forceinline__ void clha_record_error(int* err, int code, int proble
     }
 }
 
+// Kernels launched with clha_launch_overlapped may start while the kernel before them in the stream still runs:
+// before its first access to global memory every thread calls clha_wait_inputs, which returns when that kernel
+// has finished and its writes can be seen; clha_allow_next lets the kernel after this one start likewise. The
+// set-up of one call (a few microseconds for the tensor-core kernels) then runs in the tail of the call before.
+// Every block waits before it ends, so a kernel that has finished implies all before it have.
+__device__ __forceinline__ void clha_wait_inputs() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+__device__ __forceinline__ void clha_allow_next() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+
 // ------------------------------------------------------------------------------ host helpers
+// Launch of a kernel that calls clha_wait_inputs; `cluster` CTAs a cluster (1: none).
+template <typename... P, typename... A>
+cudaError_t clha_launch_overlapped(void (*kernel)(P...), unsigned grid_x, unsigned threads, size_t smem, cudaStream_t s,
+                                   unsigned cluster, const A&... args) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(grid_x);
+    cfg.blockDim = dim3(threads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = s;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = cluster;
+    attr[1].val.clusterDim.y = 1;
+    attr[1].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = cluster > 1 ? 2 : 1;
+    return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
 clha_status clha_fail(clha_ctx* ctx, clha_status st, const char* fmt, ...);
 clha_status clha_cuda_check(clha_ctx* ctx, cudaError_t e, const char* what);
 // Workspace of at least `bytes` (grows; synchronises the stream when it has to reallocate).

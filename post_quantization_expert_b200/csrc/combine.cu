@@ -47,6 +47,8 @@ __global__ void __launch_bounds__(kThreads) combine_kernel(const TZ* __restrict_
                                                            int64_t n, int k, int E, const int64_t* __restrict__ seg,
                                                            const int32_t* __restrict__ perm, const TY* __restrict__ add,
                                                            TY* __restrict__ Y, int* err) {
+    clha_allow_next();
+    clha_wait_inputs();
     extern __shared__ int64_t row_of[];                    // [k] the slots' packed rows, then [k] weights
     float* wt = reinterpret_cast<float*>(row_of + k);
     for (int64_t t = blockIdx.x; t < n; t += gridDim.x) {
@@ -95,15 +97,15 @@ cudaError_t launch_combine(cudaStream_t s, const void* Z, int z_f32, int64_t row
     const unsigned blocks = (unsigned)(n < 65536 * 16 ? n : 65536 * 16);
     const size_t smem = (size_t)k * 12;
     typedef __nv_bfloat16 bf;
-#define CLHA_CMB(TZ, TY)                                                                                            \
-    combine_kernel<TZ, TY><<<blocks, kThreads, smem, s>>>((const TZ*)Z, rows, d, ids, w, n, k, E, seg, perm,          \
-                                                         (const TY*)add, (TY*)Y, err)
-    if (z_f32) {
-        if (y_f32) CLHA_CMB(float, float); else CLHA_CMB(float, bf);
-    } else {
-        if (y_f32) CLHA_CMB(bf, float); else CLHA_CMB(bf, bf);
-    }
-#undef CLHA_CMB
+    const auto launch = [&](auto tz, auto ty) {
+        typedef decltype(tz) TZ;
+        typedef decltype(ty) TY;
+        return clha_launch_overlapped(combine_kernel<TZ, TY>, blocks, kThreads, smem, s, 1, (const TZ*)Z, rows, d, ids, w, n, k,
+                                      E, seg, perm, (const TY*)add, (TY*)Y, err);
+    };
+    const cudaError_t e = z_f32 ? (y_f32 ? launch(float(), float()) : launch(float(), bf()))
+                                : (y_f32 ? launch(bf(), float()) : launch(bf(), bf()));
+    if (e != cudaSuccess) return e;
     clha_note_launches(1);
     return cudaGetLastError();
 }

@@ -205,6 +205,8 @@ struct QuantArgs {
 
 template <typename T, int BLOCK, bool SCALED>
 __global__ void __launch_bounds__(kThreads) fp4_quantize_kernel(QuantArgs p) {
+    clha_allow_next();
+    clha_wait_inputs();
     const int lane = threadIdx.x & 31, sub = lane & 7;
     const int64_t live = p.seg ? p.seg[p.E] : p.rows;
     const int64_t slots = (min(live, p.rows) + 127) / 128 * 32;
@@ -310,10 +312,9 @@ unsigned item_blocks(int64_t items, int num_sms) {
 template <typename T, int BLOCK>
 cudaError_t launch_q(cudaStream_t s, int num_sms, const QuantArgs& p) {
     const unsigned blocks = item_blocks((p.rows + 127) / 128 * 32 * (p.d >> 7), num_sms);
-    if (p.g)
-        fp4_quantize_kernel<T, BLOCK, true><<<blocks, kThreads, 0, s>>>(p);
-    else
-        fp4_quantize_kernel<T, BLOCK, false><<<blocks, kThreads, 0, s>>>(p);
+    cudaError_t e = clha_launch_overlapped(p.g ? fp4_quantize_kernel<T, BLOCK, true> : fp4_quantize_kernel<T, BLOCK, false>,
+                                           blocks, kThreads, 0, s, 1, p);
+    if (e != cudaSuccess) return e;
     clha_note_launches(1);
     return cudaGetLastError();
 }
@@ -337,6 +338,8 @@ __global__ void __launch_bounds__(kThreads) fp4_dequantize_kernel(const uint8_t*
                                                                   const uint8_t* __restrict__ scales, int64_t rows, int d,
                                                                   const float* __restrict__ g, int64_t rows_per_g,
                                                                   int wide, void* __restrict__ out) {
+    clha_allow_next();
+    clha_wait_inputs();
     const int sub = threadIdx.x & 7;
     const int64_t slots = (rows + 127) / 128 * 32;
     const int atoms = d / BLOCK / 4;
@@ -435,17 +438,16 @@ cudaError_t launch_fp4_dequantize(cudaStream_t s, int num_sms, const uint8_t* co
                                   int d, int block, const float* g, int64_t rows_per_g, void* out, int out_f32) {
     const unsigned blocks = item_blocks((rows + 127) / 128 * 32 * (d >> 7), num_sms);
     const int wide = ((uintptr_t)out & 31) == 0;
-#define CLHA_DQ(B, F, S) \
-    fp4_dequantize_kernel<B, F, S><<<blocks, kThreads, 0, s>>>(codes, scales, rows, d, g, rows_per_g, wide, out)
-#define CLHA_DQ2(B, F) \
-    if (g) CLHA_DQ(B, F, true); else CLHA_DQ(B, F, false)
-    if (block == 32) {
-        if (out_f32) { CLHA_DQ2(32, true); } else { CLHA_DQ2(32, false); }
-    } else {
-        if (out_f32) { CLHA_DQ2(16, true); } else { CLHA_DQ2(16, false); }
-    }
-#undef CLHA_DQ2
-#undef CLHA_DQ
+    const auto kernel = [&] {
+        if (block == 32) {
+            if (out_f32) return g ? fp4_dequantize_kernel<32, true, true> : fp4_dequantize_kernel<32, true, false>;
+            return g ? fp4_dequantize_kernel<32, false, true> : fp4_dequantize_kernel<32, false, false>;
+        }
+        if (out_f32) return g ? fp4_dequantize_kernel<16, true, true> : fp4_dequantize_kernel<16, true, false>;
+        return g ? fp4_dequantize_kernel<16, false, true> : fp4_dequantize_kernel<16, false, false>;
+    }();
+    cudaError_t e = clha_launch_overlapped(kernel, blocks, kThreads, 0, s, 1, codes, scales, rows, d, g, rows_per_g, wide, out);
+    if (e != cudaSuccess) return e;
     clha_note_launches(1);
     return cudaGetLastError();
 }

@@ -141,9 +141,11 @@ fp4_matmul_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant
         tc::prefetch_tmap(&tmW);
         tc::prefetch_tmap(&tmWs);
     }
+    if (warp == 1) tc::tmem_alloc(tc::smem_u32(tmem_slot), C::TCOLS);
+    clha_allow_next();
+    clha_wait_inputs();
     if (p.seg)
         for (int i = threadIdx.x; i <= 2 * p.E; i += kThreads) seg[i] = (int)p.seg[i];
-    if (warp == 1) tc::tmem_alloc(tc::smem_u32(tmem_slot), C::TCOLS);
     tc::fence_before_sync();
     __syncthreads();
     tc::fence_after_sync();
@@ -456,6 +458,8 @@ fp4_matmul_pair_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_con
         tc::fence_barrier_init();
     }
     if (warp == 1) tc::tmem_alloc_pair(tc::smem_u32(tmem_slot), 512);
+    clha_allow_next();
+    clha_wait_inputs();
     tc::fence_before_sync();
     __syncthreads();
     tc::cluster_sync();   // both CTAs' barriers exist before any copy or arrival reaches them
@@ -692,19 +696,9 @@ cudaError_t launch_pair(cudaStream_t s, int num_sms, const Fp4Product& a, int* e
     if ((e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM)) != cudaSuccess) return e;
     const int tile_n = ACT ? 128 : 256;
     MatmulArgs p{a.rows, a.K, a.N, a.seg, a.E, a.xg, a.wg, a.ug, a.Y, (a.N + tile_n - 1) / tile_n, 1, err};
-    cudaLaunchConfig_t cfg = {};
-    cfg.blockDim = dim3(kThreads);
-    cfg.dynamicSmemBytes = C::SMEM;
-    cfg.stream = s;
-    cfg.gridDim = dim3((unsigned)(num_sms / 2 * 2));
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim.x = 2;
-    attr[0].val.clusterDim.y = 1;
-    attr[0].val.clusterDim.z = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    if ((e = cudaLaunchKernelEx(&cfg, kernel, t.X, t.Xs, t.W, t.Ws, t.U, t.Us, t.Y, p)) != cudaSuccess) return e;
+    e = clha_launch_overlapped(kernel, (unsigned)(num_sms / 2 * 2), kThreads, C::SMEM, s, 2, t.X, t.Xs, t.W, t.Ws, t.U,
+                               t.Us, t.Y, p);
+    if (e != cudaSuccess) return e;
     clha_note_launches(1);
     return cudaGetLastError();
 }
@@ -724,19 +718,10 @@ cudaError_t launch_few(cudaStream_t s, int num_sms, const Fp4Product& a, int* er
     const int nk = (a.K + 255) / 256;
     const int slots = num_sms * C::CTAS;
     while (p.split < 8 && expect * p.split * 2 <= slots && nk >= 4 * p.split) p.split *= 2;
-    cudaLaunchConfig_t cfg = {};
-    cfg.blockDim = dim3(kThreads);
-    cfg.dynamicSmemBytes = C::SMEM;
-    cfg.stream = s;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim.x = (unsigned)p.split;
-    attr[0].val.clusterDim.y = 1;
-    attr[0].val.clusterDim.z = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    cfg.gridDim = dim3((unsigned)(p.split > 1 ? bound * p.split : (bound < slots ? bound : slots)));
-    if ((e = cudaLaunchKernelEx(&cfg, kernel, t.X, t.Xs, t.W, t.Ws, t.U, t.Us, p)) != cudaSuccess) return e;
+    const int64_t grid = p.split > 1 ? bound * p.split : (bound < slots ? bound : slots);
+    e = clha_launch_overlapped(kernel, (unsigned)grid, kThreads, C::SMEM, s, (unsigned)p.split, t.X, t.Xs, t.W, t.Ws, t.U,
+                               t.Us, p);
+    if (e != cudaSuccess) return e;
     clha_note_launches(1);
     return cudaGetLastError();
 }

@@ -365,6 +365,8 @@ __device__ __noinline__ void exact_token(const GateArgs& p, int64_t t, int lane,
 
 template <typename T, int VPL>
 __global__ void __launch_bounds__(kWarps * 32) route_gated_kernel(GateArgs p, int one_block) {
+    clha_allow_next();
+    clha_wait_inputs();
     extern __shared__ int hist[];
     for (int e = threadIdx.x; e < p.E; e += blockDim.x) hist[e] = 0;
     __syncthreads();
@@ -433,6 +435,8 @@ __device__ __forceinline__ void load_run(const T* p, float (&l)[VPL]) {   // 16-
 template <typename T, int LPT, int VPL>
 __global__ void __launch_bounds__(kWarps * 32, VPL == 8 ? 4 : 2) route_lanes_kernel(GateArgs p, int one_block, int vec) {
     constexpr int TPW = 32 / LPT;                            // tokens a warp
+    clha_allow_next();
+    clha_wait_inputs();
     extern __shared__ int hist[];
     for (int e = threadIdx.x; e < p.E; e += blockDim.x) hist[e] = 0;
     __syncthreads();
@@ -594,19 +598,20 @@ cudaError_t launch_t(cudaStream_t s, int num_sms, const GateArgs& p) {
     int64_t blocks = (p.n + tokens - 1) / tokens;
     // up to two rounds of one block: it overwrites the counts, and the clearing launch is saved
     const int one = blocks <= 2;
-    if (one) {
+    cudaError_t e = cudaSuccess;
+    if (one)
         blocks = 1;
-    } else {
-        cudaError_t e = cudaMemsetAsync(p.counts, 0, p.E * sizeof(int32_t), s);
-        if (e != cudaSuccess) return e;
-    }
+    else
+        e = cudaMemsetAsync(p.counts, 0, p.E * sizeof(int32_t), s);
+    if (e != cudaSuccess) return e;
     // one wave: a block's histogram and bias serve all of its tokens
     const int64_t wave = (int64_t)num_sms * (lanes ? 4 : 8);
     if (blocks > wave) blocks = wave;
     const size_t smem = p.E * sizeof(int);
     if (lanes) {
         const int vec = p.E % 8 == 0 && ((uintptr_t)p.logits & 15) == 0;
-#define CLHA_GATE(L, V) route_lanes_kernel<T, L, V><<<(unsigned)blocks, kWarps * 32, smem, s>>>(p, one, vec)
+#define CLHA_GATE(L, V) \
+    e = clha_launch_overlapped(route_lanes_kernel<T, L, V>, (unsigned)blocks, kWarps * 32, smem, s, 1, p, one, vec)
         if (p.E <= 32) CLHA_GATE(4, 8);
         else if (p.E <= 64) CLHA_GATE(8, 8);
         else if (p.E <= 128) CLHA_GATE(16, 8);
@@ -614,7 +619,8 @@ cudaError_t launch_t(cudaStream_t s, int num_sms, const GateArgs& p) {
         else CLHA_GATE(32, 16);
 #undef CLHA_GATE
     } else {
-#define CLHA_GATE(V) route_gated_kernel<T, V><<<(unsigned)blocks, kWarps * 32, smem, s>>>(p, one)
+#define CLHA_GATE(V) \
+    e = clha_launch_overlapped(route_gated_kernel<T, V>, (unsigned)blocks, kWarps * 32, smem, s, 1, p, one)
         if (p.E <= 32) CLHA_GATE(1);
         else if (p.E <= 64) CLHA_GATE(2);
         else if (p.E <= 128) CLHA_GATE(4);
@@ -623,6 +629,7 @@ cudaError_t launch_t(cudaStream_t s, int num_sms, const GateArgs& p) {
         else CLHA_GATE(32);
 #undef CLHA_GATE
     }
+    if (e != cudaSuccess) return e;
     clha_note_launches(1);
     return cudaGetLastError();
 }
