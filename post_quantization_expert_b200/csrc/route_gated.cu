@@ -270,7 +270,8 @@ __device__ __forceinline__ uint64_t best_key(const uint64_t (&key)[N], int lane,
     return m;
 }
 
-template <typename T, int VPL>
+// VPL experts and GPL groups a lane.
+template <typename T, int VPL, int GPL>
 __device__ __noinline__ void exact_token(const GateArgs& p, int64_t t, int lane, int* hist) {
     const T* row = reinterpret_cast<const T*>(p.logits) + t * p.E;
     double s[VPL];
@@ -304,9 +305,9 @@ __device__ __noinline__ void exact_token(const GateArgs& p, int64_t t, int lane,
     }
     if (p.n_groups > 1) {
         const int size = p.E / p.n_groups;
-        uint64_t rank[VPL];                                   // of groups lane, lane + 32, ...
+        uint64_t rank[GPL];                                   // of groups lane, lane + 32, ...
 #pragma unroll
-        for (int i = 0; i < VPL; ++i) rank[i] = 0;
+        for (int i = 0; i < GPL; ++i) rank[i] = 0;
         for (int g = 0; g < p.n_groups; ++g) {
             int first, second;
             const auto inside = [&](int i) { return (unsigned)(lane + 32 * i - g * size) < (unsigned)size; };
@@ -317,7 +318,7 @@ __device__ __noinline__ void exact_token(const GateArgs& p, int64_t t, int lane,
                 r = to_key(from_key(r) + from_key(r2));
             }
 #pragma unroll
-            for (int i = 0; i < VPL; ++i)
+            for (int i = 0; i < GPL; ++i)
                 if (g == lane + 32 * i) rank[i] = r;
         }
         unsigned kept = 0;
@@ -325,7 +326,7 @@ __device__ __noinline__ void exact_token(const GateArgs& p, int64_t t, int lane,
             int g;
             best_key(rank, lane, [](int) { return true; }, g);
 #pragma unroll
-            for (int i = 0; i < VPL; ++i)
+            for (int i = 0; i < GPL; ++i)
                 if (g == lane + 32 * i) { rank[i] = 0; kept |= 1u << i; }
         }
 #pragma unroll
@@ -335,9 +336,8 @@ __device__ __noinline__ void exact_token(const GateArgs& p, int64_t t, int lane,
             if (!(who >> (g >> 5) & 1)) key[i] = 0;
         }
     }
-    double sum = 0;
-    int my_id[VPL];
-    double my_s[VPL];
+    const double scale = p.scale;
+    double sum = 0, mine = 0;                                 // the score of this lane's last choice
     for (int r = 0; r < p.k; ++r) {
         int e;
         best_key(key, lane, [](int) { return true; }, e);
@@ -347,19 +347,21 @@ __device__ __noinline__ void exact_token(const GateArgs& p, int64_t t, int lane,
             if (e == lane + 32 * i) { key[i] = 0; sv = s[i]; }
         sv = __shfl_sync(kAll, sv, e & 31);
         sum += sv;
-#pragma unroll
-        for (int i = 0; i < VPL; ++i)
-            if (r == lane + 32 * i) { my_id[i] = e; my_s[i] = sv; }
-    }
-#pragma unroll
-    for (int i = 0; i < VPL; ++i) {
-        const int j = lane + 32 * i;
-        if (j < p.k) {
-            const double w = p.renorm ? (sum > 0 ? my_s[i] / sum : 1.0 / p.k) : my_s[i];
-            p.ids[t * p.k + j] = my_id[i];
-            p.weights[t * p.k + j] = (float)(w * (double)p.scale);
-            atomicAdd(&hist[my_id[i]], 1);
+        if (lane == (r & 31)) {
+            p.ids[t * p.k + r] = e;
+            atomicAdd(&hist[e], 1);
+            mine = sv;
+            if (!p.renorm) p.weights[t * p.k + r] = (float)(sv * scale);
         }
+    }
+    if (!p.renorm) return;
+    for (int j = lane; j < p.k; j += 32) {
+        double w = mine;
+        if (j + 32 < p.k) {                                   // more than 32 choices: an earlier one's score again
+            const float l = finite_logit<T>(row, p.ids[t * p.k + j]);
+            w = p.sigmoid ? 1 / (1 + exp(-(double)l)) : exp((double)l - (double)m) / total;
+        }
+        p.weights[t * p.k + j] = (float)((sum > 0 ? w / sum : 1.0 / p.k) * scale);
     }
 }
 
@@ -382,7 +384,7 @@ __global__ void __launch_bounds__(kWarps * 32) route_gated_kernel(GateArgs p, in
         }
         if (__any_sync(kAll, bad) && lane == 0)
             clha_record_error(p.err, CLHA_ERR_NONFINITE, (int)(t & 0x7fffffff), 0, KID_GATE);
-        if (!select_token<VPL>(p, l, t, lane, hist)) exact_token<T, VPL>(p, t, lane, hist);
+        if (!select_token<VPL>(p, l, t, lane, hist)) exact_token<T, VPL, VPL>(p, t, lane, hist);
     }
     __syncthreads();
     for (int e = threadIdx.x; e < p.E; e += blockDim.x) {
@@ -576,7 +578,7 @@ __global__ void __launch_bounds__(kWarps * 32, VPL == 8 ? 4 : 2) route_lanes_ker
         while (again) {
             const int w = __ffs(again) - 1;
             again &= again - 1;
-            exact_token<T, LPT * VPL / 32 ? LPT * VPL / 32 : 1>(p, tb + w / LPT, lane, hist);
+            exact_token<T, LPT * VPL / 32 ? LPT * VPL / 32 : 1, 1>(p, tb + w / LPT, lane, hist);
         }
     }
     __syncthreads();

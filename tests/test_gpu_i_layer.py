@@ -353,6 +353,10 @@ def test_route_near_ties(ctx, score, groups, top, rank):
     same = torch.zeros((20, E))                                  # every choice equal: the lowest experts
     check_route(ctx, same, k, None, score=score, n_groups=groups, top_groups=top, group_rank=rank)
     check_route(ctx, same, k, torch.zeros(E), score=score, n_groups=groups, top_groups=top, group_rank=rank)
+    for many in ((40, 128), (70, 1000)):                         # choices above a warp's lanes
+        check_route(ctx, torch.zeros((5, many[1])), many[0], torch.zeros(many[1]), score=score)
+        check_route(ctx, torch.randn((5, many[1]), generator=gen(12)).mul(4).round().div(4), many[0],
+                    torch.zeros(many[1]), score=score, renormalise=groups == 1)
     coarse = torch.randn((64, E), generator=gen(11)).mul(2).round().div(2)   # many exact ties
     check_route(ctx, coarse, k, torch.zeros(E), score=score, n_groups=groups, top_groups=top, group_rank=rank)
 
