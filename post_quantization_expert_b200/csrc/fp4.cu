@@ -15,9 +15,10 @@
 // Both kernels stream. Eight lanes take 128 columns, 16 a lane (32 bytes of bf16 in one access, 8 bytes of
 // codes), of the four rows r, r + 32, r + 64, r + 96 of a 128-row tile: four loads in flight a lane, and the
 // scales of four blocks of those rows are 16 consecutive bytes of the tiled layout (the lanes transpose 4 x 4
-// bytes by two exchanges and store 4 bytes each). A block is one lane (16) or two (32). With 8 columns a lane, a
-// 64-bit division a step and byte-wise decoding the kernels were issue-bound: 32768 tokens x 2048 into the segments
-// of 64 experts, top 6, took 285 us (114 instructions per 8 columns) and decoding to bf16 340 us.
+// bytes by two exchanges and store 4 bytes each). A block is one lane (16) or two (32). They are issue-bound
+// rather than HBM-bound: 32768 tokens x 2048 into the segments of 64 experts, top 6, take 130 us (97 M warp
+// instructions; 8 columns a lane and a 64-bit division a step took 285 us, routed rows as they lie 142 us, runs
+// of 512 columns a unit 140 us), decoding them to bf16 180 us (86 % of the measured copy bandwidth).
 #include "clha_internal.h"
 
 #include <cuda_fp16.h>
@@ -65,7 +66,7 @@ __device__ __forceinline__ float from_e4m3(uint32_t byte) {   // byte < 0x7f: si
 __device__ __forceinline__ float pow2_byte(uint32_t byte) {   // 2^(byte - 127)
     return byte ? __uint_as_float(byte << 23) : 0x1p-127f;
 }
-__device__ __forceinline__ float max_nan(float a, float b) {
+__device__ __forceinline__ float max_nan(float a, float b) {   // NaN if one is
     float r;
     asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
     return r;
@@ -127,6 +128,37 @@ struct Raw {
     __device__ __forceinline__ float at(int i) const {       // i a constant once unrolled
         if (sizeof(T) == 4) return __uint_as_float(w[i >> 3 & (N - 1)][i & 7]);
         return __uint_as_float(i & 1 ? w[0][i >> 1] & 0xffff0000u : w[0][i >> 1] << 16);
+    }
+    // The largest magnitude; NaN if there is one.
+    __device__ __forceinline__ float largest() const {
+        if (sizeof(T) == 2) {                                // two columns an instruction, signs combined as they come
+            uint32_t m = w[0][0];
+#pragma unroll
+            for (int i = 1; i < 8; ++i) asm("max.NaN.xorsign.abs.bf16x2 %0, %0, %1;" : "+r"(m) : "r"(w[0][i]));
+            return max_nan(fabsf(__uint_as_float(m << 16)), fabsf(__uint_as_float(m & 0xffff0000u)));
+        }
+        float m = 0.f;
+#pragma unroll
+        for (int i = 0; i < 16; ++i) m = max_nan(m, fabsf(at(i)));
+        return m;
+    }
+    // Columns 8 h .. 8 h + 7 times r. A power of two leaves a bfloat16 exact (or far below the smallest code): two
+    // products an instruction, before they are taken apart.
+    __device__ __forceinline__ void times(int h, float r, bool pow2, float (&t)[8]) const {
+        if (sizeof(T) == 2 && pow2) {
+            const __nv_bfloat162 rr = __float2bfloat162_rn(r);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                uint32_t v = w[0][4 * h + i];
+                const __nv_bfloat162 m = __hmul2(*reinterpret_cast<__nv_bfloat162*>(&v), rr);
+                v = *reinterpret_cast<const uint32_t*>(&m);
+                t[2 * i] = __uint_as_float(v << 16);
+                t[2 * i + 1] = __uint_as_float(v & 0xffff0000u);
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) t[i] = at(8 * h + i) * r;
+        }
     }
 };
 
@@ -200,106 +232,151 @@ struct QuantArgs {
     uint8_t* codes;
     uint8_t* scales;
     int wide;                     // X is 32-byte aligned
+    int bands;                    // 1: row tiles as they lie
+    int run;                      // columns of a work unit
     int* err;
 };
 
+// Routed rows of a large X in the order of its tokens: a token's rows lie in k segments, so that row tiles taken as
+// they lie read X from DRAM once for each (of 726 MB moved for 32768 tokens x 2048 in six experts each, 134 were X once).
+// Segments list their tokens in ascending order: the tiles are taken in bands, first the first 1 / bands of every
+// segment, and a band's share of X stays in L2. before[b E + e]: the tiles before band b of expert e.
+constexpr int kBandEntries = 2048;
+__device__ void band_table(const QuantArgs& p, int* before) {
+    __shared__ int sums[kThreads];
+    const int entries = p.bands * p.E, per = (entries + kThreads - 1) / kThreads;
+    const int lo = threadIdx.x * per, hi = min(entries, lo + per);
+    int sum = 0;
+    for (int i = lo; i < hi; ++i) {
+        const int b = i / p.E, e = i - b * p.E;
+        const int64_t tiles = (p.seg[e + 1] - p.seg[e]) >> 7;
+        before[i] = sum;
+        sum += (int)(tiles * (b + 1) / p.bands - tiles * b / p.bands);
+    }
+    sums[threadIdx.x] = sum;
+    __syncthreads();
+    for (int o = 1; o < kThreads; o <<= 1) {
+        const int v = threadIdx.x >= o ? sums[threadIdx.x - o] : 0;
+        __syncthreads();
+        sums[threadIdx.x] += v;
+        __syncthreads();
+    }
+    for (int i = lo; i < hi; ++i) before[i] += sums[threadIdx.x] - sum;
+    __syncthreads();
+}
+// The row tile that is taken w-th.
+__device__ __forceinline__ int64_t banded(const QuantArgs& p, const int* before, int64_t w) {
+    int lo = 0, hi = p.bands * p.E - 1;
+    while (lo < hi) {                                        // the last entry with before <= w (empty ones share theirs)
+        const int mid = (lo + hi + 1) >> 1;
+        if (before[mid] <= w) lo = mid; else hi = mid - 1;
+    }
+    const int b = lo / p.E, e = lo - b * p.E;
+    const int64_t first = p.seg[e] >> 7, tiles = (p.seg[e + 1] >> 7) - first;
+    return first + tiles * b / p.bands + (w - before[lo]);
+}
+
 template <typename T, int BLOCK, bool SCALED>
-__global__ void __launch_bounds__(kThreads) fp4_quantize_kernel(QuantArgs p) {
+__global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 4 : 2) fp4_quantize_kernel(QuantArgs p) {
     clha_allow_next();
     clha_wait_inputs();
-    const int lane = threadIdx.x & 31, sub = lane & 7;
-    const int64_t live = p.seg ? p.seg[p.E] : p.rows;
-    const int64_t slots = (min(live, p.rows) + 127) / 128 * 32;
+    const int sub = threadIdx.x & 7, r = threadIdx.x >> 3;
+    const int64_t live = p.seg ? min(p.seg[p.E], p.rows) : p.rows;
     constexpr int LPB = BLOCK / 16;                          // lanes a block
     const int atoms = p.d / BLOCK / 4;                       // 512-byte scale tiles across a row tile
-    Items it(p.d >> 7);
-    // whole warps leave together: the lanes of one exchange values
-    for (; __any_sync(0xffffffffu, it.slot < slots); it.next()) {
-        const bool work = it.slot < slots;
-        const int64_t r0 = (it.slot >> 5) * 128 + (it.slot & 31);
-        const int c = it.chunk * 128 + sub * 16;
-        Raw<T> x[4];
-        bool has[4];
+    extern __shared__ int before[];
+    if (p.bands > 1) band_table(p, before);
+    // a unit: the 128 rows of a tile, rows r, r + 32, r + 64, r + 96 to eight lanes, by p.run columns
+    const int runs = (p.d + p.run - 1) / p.run;
+    for (int64_t u = blockIdx.x;; u += gridDim.x) {
+        int64_t tile = u / runs;
+        const int c0 = (int)(u - tile * runs) * p.run, c1 = min(p.d, c0 + p.run);
+        if (tile * 128 >= live) break;
+        if (p.bands > 1) tile = banded(p, before, tile);
+        const int64_t r0 = tile * 128 + r;
+        const T* src[4];                                       // null: a row of zeros
+        uint8_t* dst[4];                                       // null: behind the last row
 #pragma unroll
         for (int a = 0; a < 4; ++a) {
             const int64_t row = r0 + 32 * a;
-            has[a] = work && row < live && row < p.rows;
-            int64_t src = row;
-            if (p.perm) src = has[a] ? p.perm[row] : -1;
-            if (has[a] && src >= p.n) {
-                clha_record_error(p.err, CLHA_ERR_INVALID_ARG, (int)(row & 0x7fffffff), (int)src, KID_FP4);
-                src = -1;
+            const bool has = row < live;
+            int64_t at = has ? row : -1;
+            if (has && p.perm) at = p.perm[row];
+            if (at >= p.n) {
+                clha_record_error(p.err, CLHA_ERR_INVALID_ARG, (int)(row & 0x7fffffff), (int)at, KID_FP4);
+                at = -1;
             }
-            if (has[a] && src >= 0)
-                x[a].load(reinterpret_cast<const T*>(p.X) + src * p.d + c, p.wide);
-            else
-                x[a].zero();
+            src[a] = at >= 0 ? reinterpret_cast<const T*>(p.X) + at * p.d : nullptr;
+            dst[a] = has ? p.codes + row * (p.d >> 1) : nullptr;
         }
-        uint32_t sb = 0;                                     // the four rows' scale bytes of this lane's block
+        for (int c = c0 + sub * 16; c < c1; c += 128) {
+            Raw<T> x[4];
 #pragma unroll
-        for (int a = 0; a < 4; ++a) {
-            const int64_t row = r0 + 32 * a;
-            float g = 1.f;
-            if (SCALED) {
-                if (has[a]) g = __ldg(p.g + row / p.rows_per_g);
-                if (!(g > 0.f && g < INFINITY)) {
-                    clha_record_error(p.err, CLHA_ERR_INVALID_ARG, (int)(row & 0x7fffffff), 0, KID_FP4);
-                    g = 1.f;
-                }
+            for (int a = 0; a < 4; ++a) {
+                if (src[a])
+                    x[a].load(src[a] + c, p.wide);
+                else
+                    x[a].zero();
             }
-            // outside this range a reciprocal may be subnormal and short of bits: NaN sends every decision to float64
-            const float rg = !SCALED ? 1.f : g > 0x1p-100f && g < 0x1p100f ? 1.f / g : NAN;
-            const float r6g = rg * (1.f / 6.f);
-            float top = 0.f;
+            uint32_t sb = 0;                                     // the four rows' scale bytes of this lane's block
 #pragma unroll
-            for (int i = 0; i < 16; ++i) top = max_nan(top, fabsf(x[a].at(i)));
-            if (LPB == 2) top = max_nan(top, __shfl_xor_sync(0xffffffffu, top, 1));
-            uint32_t q[2] = {0u, 0u}, byte;
-            if (!(top < INFINITY)) {                         // the same decision in both lanes of a block
-                clha_record_error(p.err, CLHA_ERR_NONFINITE, (int)(row & 0x7fffffff), c, KID_FP4);
-                byte = BLOCK == 32 ? 0xff : 0x7f;            // the formats' NaN
-            } else {
-                float r;
-                byte = block_scale<BLOCK, SCALED>(top, g, rg, r6g, &r);
+            for (int a = 0; a < 4; ++a) {
+                const int64_t row = r0 + 32 * a;
+                float g = 1.f;
+                if (SCALED) {
+                    if (dst[a]) g = __ldg(p.g + row / p.rows_per_g);
+                    if (!(g > 0.f && g < INFINITY)) {
+                        clha_record_error(p.err, CLHA_ERR_INVALID_ARG, (int)(row & 0x7fffffff), 0, KID_FP4);
+                        g = 1.f;
+                    }
+                }
+                // outside this range a reciprocal may be subnormal and short of bits: NaN sends every decision to float64
+                const float rg = !SCALED ? 1.f : g > 0x1p-100f && g < 0x1p100f ? 1.f / g : NAN;
+                const float r6g = rg * (1.f / 6.f);
+                float top = x[a].largest();
+                if (LPB == 2) top = max_nan(top, __shfl_xor_sync(0xffffffffu, top, 1));
+                uint32_t q[2] = {0u, 0u}, byte;
+                if (!(top < INFINITY)) {                         // the same decision in both lanes of a block
+                    clha_record_error(p.err, CLHA_ERR_NONFINITE, (int)(row & 0x7fffffff), c, KID_FP4);
+                    byte = BLOCK == 32 ? 0xff : 0x7f;            // the formats' NaN
+                } else {
+                    float r;
+                    byte = block_scale<BLOCK, SCALED>(top, g, rg, r6g, &r);
 #pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    float t[8];
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) t[i] = x[a].at(8 * h + i) * r;
-                    if (BLOCK == 32 && !SCALED) {
+                    for (int h = 0; h < 2; ++h) {
+                        float t[8];
+                        x[a].times(h, r, BLOCK == 32 && !SCALED, t);
                         q[h] = e2m1x8(t);
-                        continue;
-                    }
-                    float lo[8], hi[8];
+                        if (BLOCK == 32 && !SCALED) continue;
+                        float lo[8], hi[8];
 #pragma unroll
-                    for (int i = 0; i < 8; ++i) {
-                        lo[i] = t[i] * kLo;
-                        hi[i] = t[i] * kHi;
-                    }
-                    q[h] = e2m1x8(lo);
-                    if (q[h] != e2m1x8(hi) || (r != 0.f && !(r > 0x1p-100f && r < 0x1p100f))) {
-                        const double dd = (BLOCK == 32 ? ldexp(1.0, (int)byte - 127) : (double)from_e4m3(byte)) * (double)g;
-                        q[h] = 0;
-                        if (dd > 0.0)
+                        for (int i = 0; i < 8; ++i) {
+                            lo[i] = t[i] * kLo;
+                            hi[i] = t[i] * kHi;
+                        }
+                        if (e2m1x8(lo) != e2m1x8(hi) || (r != 0.f && !(r > 0x1p-100f && r < 0x1p100f))) {
+                            const double dd = (BLOCK == 32 ? ldexp(1.0, (int)byte - 127) : (double)from_e4m3(byte)) * (double)g;
+                            q[h] = 0;
+                            if (dd > 0.0)
 #pragma unroll
-                            for (int i = 0; i < 8; ++i) q[h] |= e2m1_exact(x[a].at(8 * h + i), dd) << (4 * i);
+                                for (int i = 0; i < 8; ++i) q[h] |= e2m1_exact(x[a].at(8 * h + i), dd) << (4 * i);
+                        }
                     }
                 }
+                if (dst[a]) {
+                    *reinterpret_cast<uint2*>(dst[a] + (c >> 1)) = make_uint2(q[0], q[1]);
+                    sb |= byte << (8 * a);
+                }
             }
-            if (has[a]) {
-                *reinterpret_cast<uint2*>(p.codes + row * (p.d >> 1) + (c >> 1)) = make_uint2(q[0], q[1]);
-                sb |= byte << (8 * a);
-            }
+            // lane b of a tile's four blocks holds the bytes of rows 0..3 (32 apart); exchange: it gets row b's four blocks
+            const int b = sub / LPB & 3;
+            uint32_t o = __shfl_xor_sync(0xffffffffu, sb, LPB);
+            sb = b & 1 ? __byte_perm(sb, o, 0x3715) : __byte_perm(sb, o, 0x6240);
+            o = __shfl_xor_sync(0xffffffffu, sb, 2 * LPB);
+            sb = b & 2 ? __byte_perm(sb, o, 0x3276) : __byte_perm(sb, o, 0x5410);
+            if (LPB == 1 || !(sub & 1))
+                *reinterpret_cast<uint32_t*>(p.scales + ((tile * atoms + c / (4 * BLOCK)) * 32 + r) * 16 + 4 * b) = sb;
         }
-        // lane b of a tile's four blocks holds the bytes of rows 0..3 (32 apart); exchange: it gets row b's four blocks
-        const int b = sub / LPB & 3;
-        uint32_t o = __shfl_xor_sync(0xffffffffu, sb, LPB);
-        sb = b & 1 ? __byte_perm(sb, o, 0x3715) : __byte_perm(sb, o, 0x6240);
-        o = __shfl_xor_sync(0xffffffffu, sb, 2 * LPB);
-        sb = b & 2 ? __byte_perm(sb, o, 0x3276) : __byte_perm(sb, o, 0x5410);
-        if (work && (LPB == 1 || !(sub & 1)))
-            *reinterpret_cast<uint32_t*>(p.scales + (((it.slot >> 5) * atoms + c / (4 * BLOCK)) * 32 + (it.slot & 31)) * 16 +
-                                         4 * b) = sb;
     }
 }
 
@@ -311,9 +388,10 @@ unsigned item_blocks(int64_t items, int num_sms) {
 
 template <typename T, int BLOCK>
 cudaError_t launch_q(cudaStream_t s, int num_sms, const QuantArgs& p) {
-    const unsigned blocks = item_blocks((p.rows + 127) / 128 * 32 * (p.d >> 7), num_sms);
+    const int64_t units = (p.rows + 127) / 128 * ((p.d + p.run - 1) / p.run), most = (int64_t)num_sms * (sizeof(T) == 2 ? 4 : 2);
+    const unsigned blocks = (unsigned)(units < most ? units : most);
     cudaError_t e = clha_launch_overlapped(p.g ? fp4_quantize_kernel<T, BLOCK, true> : fp4_quantize_kernel<T, BLOCK, false>,
-                                           blocks, kThreads, 0, s, 1, p);
+                                           blocks, kThreads, p.bands > 1 ? p.bands * p.E * 4 : 0, s, 1, p);
     if (e != cudaSuccess) return e;
     clha_note_launches(1);
     return cudaGetLastError();
@@ -429,7 +507,15 @@ __global__ void fp4_finish_scale_kernel(uint32_t* top, int batch, float largest,
 cudaError_t launch_fp4_quantize(cudaStream_t s, int num_sms, const void* X, int x_f32, int64_t n, int d,
                                 const int32_t* perm, int64_t rows, const int64_t* seg, int E, int block, const float* g,
                                 int64_t rows_per_g, uint8_t* codes, uint8_t* scales, int* err) {
-    const QuantArgs p{X, n, rows, d, perm, seg, E, g, rows_per_g, codes, scales, ((uintptr_t)X & 31) == 0, err};
+    // bands of X of at most 24 MB, where that leaves something to gain
+    const int64_t bytes = n * d * (x_f32 ? 4 : 2), want = (bytes + (24 << 20) - 1) / (24 << 20);
+    const int most = kBandEntries / E < 8 ? kBandEntries / E : 8;
+    const int bands = perm && seg && rows > n ? (int)(want < most ? want : most) : 1;
+    // long runs save work for each row; a few thousand units keep every SM busy
+    int run = 1024;
+    while (run > 128 && (rows + 127) / 128 * ((d + run - 1) / run) < (int64_t)num_sms * 16) run /= 2;
+    const QuantArgs p{X,     n,      rows, d,  perm, seg, E, g, rows_per_g, codes, scales, ((uintptr_t)X & 31) == 0,
+                      bands, run, err};
     if (x_f32) return block == 32 ? launch_q<float, 32>(s, num_sms, p) : launch_q<float, 16>(s, num_sms, p);
     return block == 32 ? launch_q<__nv_bfloat16, 32>(s, num_sms, p) : launch_q<__nv_bfloat16, 16>(s, num_sms, p);
 }

@@ -122,6 +122,24 @@ def test_quantize_routed_rows(ctx, fmt):
 
 
 @pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("n,E,k,d,dtype", [(9000, 24, 3, 4096, BF16), (3300, 300, 4, 2048, F32), (7000, 64, 2, 1024, F32)])
+def test_quantize_routed_rows_of_a_large_x(ctx, fmt, n, E, k, d, dtype):
+    """X of several tens of megabytes: the row tiles are taken in another order, with the same result."""
+    ids, seg, perm = route(n, E, k, 5)
+    P, end = len(perm), int(seg[E])
+    x = torch.randn((n, d), generator=torch.Generator(device=DEV).manual_seed(1), device=DEV).to(dtype)
+    codes, scales = buffers(fmt, P, d)
+    L.clha_fp4_quantize(ctx, x, n, d, FMT[fmt], codes, scales, perm=torch.from_numpy(perm).to(DEV), rows=P,
+                        seg=torch.from_numpy(seg).to(DEV), E=E)
+    p = torch.from_numpy(perm[:end]).to(DEV)
+    xp = torch.where((p >= 0)[:, None], x[p.clamp_min(0).long()], torch.zeros((), dtype=dtype, device=DEV))
+    want_c, want_s = quantize(ctx, xp, fmt)                # rows as they lie, held to the oracle above
+    assert torch.equal(codes[:end], want_c) and torch.equal(scales[:want_s.numel()], want_s)
+    assert (codes[end:] == 0xA5).all() and (scales[want_s.numel():] == 0xA5).all()
+    L.clha_check(ctx)
+
+
+@pytest.mark.parametrize("fmt", FMTS)
 def test_quantize_batch_of_scales_and_dequantize(ctx, fmt):
     """Three matrices with a scale each: clha_fp4_tensor_scale, the codes under them, and their values."""
     B, rows, d = 3, 130, 256
