@@ -235,7 +235,9 @@ def stacked(w, E):
 @pytest.mark.parametrize("n,E,k,K,N", [(300, 10, 3, 384, 256), (5, 16, 2, 512, 128), (1, 4, 1, 128, 384),
                                        (1500, 4, 2, 256, 640),
                                        # many tiles: pairs of SMs, segments with an odd number of 128-row tiles
-                                       (3001, 10, 3, 384, 640), (2000, 64, 6, 256, 384)])
+                                       (3001, 10, 3, 384, 640), (2000, 64, 6, 256, 384),
+                                       # the most experts
+                                       (1100, 1024, 130, 128, 128)])
 def test_expert_products(ctx, fmt, scaled, n, E, k, K, N):
     """Both products over segments: padding rows zero, rows behind the last segment untouched, experts without
     tokens, a scale for each expert."""
