@@ -442,13 +442,13 @@ CLHA_API clha_status clha_fp4_expert_act(clha_ctx* ctx, clha_fp4_format format, 
 
 /* Y[t] = add[t] + sum_j weights[t, j] Z[row of token t in the segment of expert ids[t, j]], j ascending, in
  * float32, for n tokens (n < 2^31). Z [rows, d] (f32 or bf16) is in the segment layout of perm and seg, which
- * clha_gather wrote for these ids; weights float32 [n, k] (NULL: all 1); add [n, d] of Y's type, or NULL; it
- * may be Y itself. A slot whose token is not in its expert's segment is recorded as CLHA_ERR_INVALID_ARG
+ * clha_gather wrote for these ids; weights float32 [n, k] (NULL: all 1); add [n, d] (f32 or bf16), or NULL;
+ * it may be Y itself, in Y's type. A slot whose token is not in its expert's segment is recorded as CLHA_ERR_INVALID_ARG
  * and adds nothing. d a multiple of 128; Z, add and Y 16-byte aligned. */
 CLHA_API clha_status clha_combine(clha_ctx* ctx, const void* Z, clha_dtype z_dtype, int64_t rows, int d,
                                   const int32_t* ids, const float* weights, int64_t n, int k, int E,
-                                  const int64_t* seg, const int32_t* perm, const void* add, void* Y,
-                                  clha_dtype y_dtype);
+                                  const int64_t* seg, const int32_t* perm, const void* add, clha_dtype add_dtype,
+                                  void* Y, clha_dtype y_dtype);
 
 /* ------------------------------------------------------------------------------ analysis */
 

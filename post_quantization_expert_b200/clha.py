@@ -129,7 +129,7 @@ def load(path: str = LIB_PATH):
         "clha_fp4_dequantize": (i32, [vp, vp, vp, i64, i32, i32, vp, i64, vp, i32]),
         "clha_fp4_matmul": (i32, [vp, i32, vp, vp, vp, i64, i32, vp, i32, vp, vp, vp, i32, vp, i32]),
         "clha_fp4_expert_act": (i32, [vp, i32, vp, vp, vp, i64, i32, vp, i32, vp, vp, vp, vp, vp, vp, i32, vp]),
-        "clha_combine": (i32, [vp, vp, i32, i64, i32, vp, vp, i64, i32, i32, vp, vp, vp, vp, i32]),
+        "clha_combine": (i32, [vp, vp, i32, i64, i32, vp, vp, i64, i32, i32, vp, vp, vp, i32, vp, i32]),
     }
     for name, (res, args) in sig.items():
         fn = getattr(lib, name)
@@ -539,11 +539,12 @@ def clha_fp4_expert_act(ctx: Context, fmt: int, x_codes, x_scales, rows: int, d_
 
 
 def clha_combine(ctx: Context, Z, rows: int, d: int, ids, weights, n: int, k: int, E: int, seg, perm, Y, add=None):
-    """Y [n, d] = add + sum_j weights[:, j] * (the row of Z that holds the token in expert ids[:, j]'s segment)."""
+    """Y [n, d] = add + sum_j weights[:, j] * (the row of Z that holds the token in expert ids[:, j]'s segment); Z, add
+    and Y float32 or bfloat16 each."""
     call, dev = "clha_combine", _device(ctx)
     zp, zt = _float_arg(call, dev, "Z", Z, rows * d)
     yp, yt = _float_arg(call, dev, "Y", Y, n * d)
     ip, wp = _arg(call, dev, "ids", ids, n * k, torch.int32), _arg(call, dev, "weights", weights, n * k, torch.float32)
     sp, pp = _arg(call, dev, "seg", seg, 2 * E + 1, torch.int64), _arg(call, dev, "perm", perm, rows, torch.int32)
-    ap = _arg(call, dev, "add", add, n * d, Y.dtype)
-    ctx._check(load().clha_combine(ctx.handle, zp, zt, rows, d, ip, wp, n, k, E, sp, pp, ap, yp, yt))
+    ap, at = (None, yt) if add is None else _float_arg(call, dev, "add", add, n * d)
+    ctx._check(load().clha_combine(ctx.handle, zp, zt, rows, d, ip, wp, n, k, E, sp, pp, ap, at, yp, yt))

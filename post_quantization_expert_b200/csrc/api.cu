@@ -826,10 +826,11 @@ extern "C" clha_status clha_fp4_expert_act(clha_ctx* ctx, clha_fp4_format format
 
 extern "C" clha_status clha_combine(clha_ctx* ctx, const void* Z, clha_dtype z_dtype, int64_t rows, int d,
                                     const int32_t* ids, const float* weights, int64_t n, int k, int E,
-                                    const int64_t* seg, const int32_t* perm, const void* add, void* Y,
-                                    clha_dtype y_dtype) {
+                                    const int64_t* seg, const int32_t* perm, const void* add,
+                                    clha_dtype add_dtype, void* Y, clha_dtype y_dtype) {
     CHECK_CTX(ctx);
-    REQUIRE(dtype_size(z_dtype) && dtype_size(y_dtype), CLHA_ERR_INVALID_ARG, "clha_combine: unknown dtype");
+    REQUIRE(dtype_size(z_dtype) && dtype_size(y_dtype) && (!add || dtype_size(add_dtype)), CLHA_ERR_INVALID_ARG,
+            "clha_combine: unknown dtype");
     REQUIRE(n >= 0 && n < (int64_t)1 << 31 && rows >= 0 && d > 0, CLHA_ERR_INVALID_ARG, "clha_combine: bad sizes");
     REQUIRE(E >= 1 && E <= 1024 && k >= 1 && k <= E, CLHA_ERR_INVALID_ARG, "clha_combine: need 1 <= k <= E <= 1024");
     REQUIRE(d % 128 == 0, CLHA_ERR_UNSUPPORTED_SHAPE, "clha_combine: d=%d is not a multiple of 128", d);
@@ -839,8 +840,8 @@ extern "C" clha_status clha_combine(clha_ctx* ctx, const void* Z, clha_dtype z_d
             "clha_combine: Z, add and Y must be 16-byte aligned");
     SET_DEVICE(ctx);
     LaunchScope launch_scope(ctx);
-    CUDA_TRY(launch_combine(ctx->stream, Z, z_dtype == CLHA_F32, rows, d, ids, weights, n, k, E, seg, perm, add, Y,
-                            y_dtype == CLHA_F32, ctx->d_err),
+    CUDA_TRY(launch_combine(ctx->stream, Z, z_dtype == CLHA_F32, rows, d, ids, weights, n, k, E, seg, perm, add,
+                            add_dtype == CLHA_F32, Y, y_dtype == CLHA_F32, ctx->d_err),
              "clha_combine");
     return CLHA_OK;
 }

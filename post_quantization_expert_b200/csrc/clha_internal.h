@@ -200,4 +200,4 @@ struct Fp4Product {
 cudaError_t launch_fp4_matmul(cudaStream_t s, int num_sms, const Fp4Product& a, int block, int y_f32, int* err);
 cudaError_t launch_combine(cudaStream_t s, const void* Z, int z_f32, int64_t rows, int d, const int32_t* ids,
                            const float* w, int64_t n, int k, int E, const int64_t* seg, const int32_t* perm,
-                           const void* add, void* Y, int y_f32, int* err);
+                           const void* add, int add_f32, void* Y, int y_f32, int* err);

@@ -509,8 +509,12 @@ cudaError_t launch_fp4_quantize(cudaStream_t s, int num_sms, const void* X, int 
                                 int64_t rows_per_g, uint8_t* codes, uint8_t* scales, int* err) {
     // bands of X of at most 24 MB, where that leaves something to gain
     const int64_t bytes = n * d * (x_f32 ? 4 : 2), want = (bytes + (24 << 20) - 1) / (24 << 20);
-    const int most = kBandEntries / E < 8 ? kBandEntries / E : 8;
-    const int bands = perm && seg && rows > n ? (int)(want < most ? want : most) : 1;
+    int bands = 1;
+    if (perm && seg && rows > n) {                            // (E is in 1..1024 then)
+        const int most = kBandEntries / E < 8 ? kBandEntries / E : 8;
+        bands = (int)(want < most ? want : most);
+        if (bands < 1) bands = 1;
+    }
     // long runs save work for each row; a few thousand units keep every SM busy
     int run = 1024;
     while (run > 128 && (rows + 127) / 128 * ((d + run - 1) / run) < (int64_t)num_sms * 16) run /= 2;

@@ -12,8 +12,9 @@
 // lane, log2(lanes) exchanges, a vote for the first lane that has it, and a scan of the winner's 8 values.
 // Groups fit this where a group is a power of two of whole lanes; other group sizes, more than 512 experts, and
 // k above twice the lanes take the general kernel (a warp a token, lane i holds experts i, i + 32, ...).
-// 32768 tokens x 64 experts, top 6: general 44 us, this one ROUTE_E64; 9973 x 256 in 8 groups, top 8: general 87 us,
-// this one ROUTE_WIDE.
+// 32768 tokens x 64 experts, top 6: general kernel 44 us, this one 16 us (about 10 of them the two launches, the
+// counters' clearing and the kernel); 9973 x 256 in 8 groups, top 8, with a bias: general 87 us, this one 32 us
+// (23 us in float32 alone).
 //
 // The order of the choices is that of exact arithmetic to float64's precision, although they are float32
 // here: two choices nearer than the float32 error bound (see `choice_slack`) make a warp repeat the token's
@@ -241,7 +242,7 @@ __device__ __forceinline__ float finite_logit(const T* row, int e) {
 // Taken by a warp for a token whose float32 choices leave a decision open: a token in thousands, but its
 // latency is the kernel's tail, so the doubles are compared as ordered 64-bit integers, whose warp-wide
 // maximum is two integer reductions (9973 x 256 experts with one such token: 24 us more as a selection by
-// exchanged doubles, EXACT_TAIL this way).
+// exchanged doubles, 9 us more this way).
 __device__ __forceinline__ uint64_t to_key(double v) {        // larger value, larger key; never 0
     const int64_t b = __double_as_longlong(v + 0.0);          // one zero
     return b < 0 ? ~(uint64_t)b : (uint64_t)b | 0x8000000000000000ull;

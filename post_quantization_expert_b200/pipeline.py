@@ -669,6 +669,7 @@ class Fp4Layer:
             self.sx = self._operand(max_tokens, dm)
             self.sh = torch.empty((max_tokens, ns * sdff), dtype=torch.bfloat16, device=dev)
             self.shq = self._operand(max_tokens, ns * sdff)
+            self.sy = torch.empty((max_tokens, dm), dtype=torch.float32, device=dev)
 
     def _operand(self, rows: int, d: int):
         """Code and scale buffers of [rows, d]."""
@@ -709,13 +710,13 @@ class Fp4Layer:
             L.clha_fp4_matmul(ctx, fmt, *self.hq, P, dff, d, ds, dm, self.z, w_scale=gd, **seg)
         add = None
         if self.shared:
-            sd, add = self.shared, Y
+            sd, add = self.shared, self.sy[:n]
             (g, gs, gg), (u, us, gu), (d, ds, gd) = *self.s_gate_up, self.s_down
             with t.span("shared"):
                 L.clha_fp4_quantize(ctx, X, n, dm, fmt, *self.sx)
                 L.clha_fp4_expert_act(ctx, fmt, *self.sx, n, dm, g, gs, u, us, sd, self.sh, g_scale=gg, u_scale=gu)
                 L.clha_fp4_quantize(ctx, self.sh, n, sd, fmt, *self.shq)
-                L.clha_fp4_matmul(ctx, fmt, *self.shq, n, sd, d, ds, dm, Y, w_scale=gd)
+                L.clha_fp4_matmul(ctx, fmt, *self.shq, n, sd, d, ds, dm, add, w_scale=gd)
         with t.span("combine"):
             L.clha_combine(ctx, self.z, P, dm, ids, weights, n, k, E, self.seg, self.perm, Y, add=add)
         return Y

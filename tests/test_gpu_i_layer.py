@@ -429,10 +429,30 @@ def test_combine(ctx, zt, yt, n, E, k, d, weighted, added):
     tol = (k + 1) * 2.0 ** -24 * mags      # one rounding for each fused multiply-add
     err = np.abs(to64(y) - want)
     assert (err <= tol + (np.abs(want) + tol) * (2.0 ** -8 if yt == BF16 else 0)).all()
-    if added:                              # add may be the output itself
+    if added:                              # an addend of the other type; one that is the output itself
+        other = F32 if yt == BF16 else BF16
+        y3 = torch.full((n, d), 5.0, dtype=yt, device=DEV)
+        L.clha_combine(ctx, *args, y3, add=dev(add.to(other)))
+        want3 = O.combine(to64(z), ids, w64, seg, perm, E, to64(add.to(other)))
+        assert (np.abs(to64(y3) - want3) <= tol * 1.01 + (np.abs(want3) + tol) * (2.0 ** -8 if yt == BF16 else 0)).all()
         y2 = dev(add).clone()
         L.clha_combine(ctx, *args, y2, add=y2)
         assert torch.equal(y2, y)
+    L.clha_check(ctx)
+
+
+def test_combine_with_an_expert_twice(ctx):
+    """A token that names one expert in two slots has two equal rows there; each slot counts."""
+    n, E, d = 40, 3, 256
+    ids = np.stack([np.arange(n) % E, np.where(np.arange(n) % 2, np.arange(n) % E, (np.arange(n) + 1) % E)], 1).astype(np.int32)
+    x = torch.randn((n, d), generator=gen(1)).to(DEV)
+    P = L.clha_packed_rows(n, 2, E)
+    seg, perm = torch.empty(2 * E + 1, dtype=torch.int64, device=DEV), torch.empty(P, dtype=torch.int32, device=DEV)
+    z = torch.empty((P, d), device=DEV)
+    L.clha_gather(ctx, x, n, d, torch.from_numpy(ids).to(DEV), 2, E, z, P, seg, perm)
+    y = torch.empty((n, d), device=DEV)
+    L.clha_combine(ctx, z, P, d, torch.from_numpy(ids).to(DEV), None, n, 2, E, seg, perm, y)
+    assert torch.equal(y, 2 * x)
     L.clha_check(ctx)
 
 
@@ -596,6 +616,14 @@ def test_layer(ctx, fmt, n, E, k, dm, dff, ns, sdff):
     assert (np.abs(to64(Y) - want) <= tol + 1e-30).all()
     with pytest.raises(ValueError):
         layer.forward(X.to(DEV).repeat(2 * (n + 6) // n + 1, 1), lg.to(DEV), Y)
+    one = torch.full((1, dm), 5.0, device=DEV)      # fewer tokens after more: the buffers hold the earlier call's rows
+    layer.forward(X[:1].to(DEV).contiguous(), lg[:1].to(DEV).contiguous(), one)
+    fresh = Fp4Layer(ctx, to_dev(w), k, max_tokens=1, fmt=FMT[fmt], score=L.SCORE_SIGMOID, scale=1.5)
+    assert torch.equal(one, fresh.forward(X[:1].to(DEV).contiguous(), lg[:1].to(DEV).contiguous(), torch.empty_like(one)))
+    empty = torch.empty((0, dm), device=DEV)
+    layer.forward(empty, torch.empty((0, E), device=DEV), empty)
+    assert (layer.counts == 0).all()
+    L.clha_check(ctx)
 
 
 def test_layer_captured_and_on_other_streams(ctx):
@@ -643,3 +671,34 @@ def test_layer_captured_and_on_other_streams(ctx):
     del graphs, g
     c1.close()
     c2.close()
+
+
+def test_offsets_past_32_bits(ctx):
+    """Codes, scales, values and outputs whose element offsets pass 2^31: the last rows against a small call."""
+    rows, d, f = 131329, 16384, L.FP4_E8M0_32          # 2.15e9 elements
+    x = torch.empty((rows, d), dtype=BF16, device=DEV)
+    x[:-300] = 1.0
+    x[-300:] = torch.randn((300, d), generator=gen(8)).to(BF16).to(DEV)
+    codes = torch.empty((rows, d // 2), dtype=torch.uint8, device=DEV)
+    scales = torch.empty(L.clha_fp4_scale_bytes(f, rows, d), dtype=torch.uint8, device=DEV)
+    L.clha_fp4_quantize(ctx, x, rows, d, f, codes, scales)
+    tail = x[-257:].contiguous()                       # 131072 = 1024 * 128: the same places in their tiles
+    wc, wsc = quantize(ctx, tail, "e8m0_32")
+    assert torch.equal(codes[-257:], wc) and torch.equal(scales[-wsc.numel():], wsc)
+    L.clha_fp4_dequantize(ctx, codes, scales, rows, d, f, x)
+    v = torch.empty((257, d), dtype=BF16, device=DEV)
+    L.clha_fp4_dequantize(ctx, wc, wsc, 257, d, f, v)
+    assert torch.equal(x[-257:], v)
+    del x
+    w = torch.randn((16384 + 128, 128), generator=gen(9))
+    wq, ws = quantize(ctx, w.to(DEV), "e8m0_32")       # Y [rows, 16512]: 2.17e9 elements
+    xq, xs = codes[:, :64].contiguous(), None
+    xs = torch.full((L.clha_fp4_scale_bytes(f, rows, 128),), 127, dtype=torch.uint8, device=DEV)
+    y = torch.empty((rows, 16512), dtype=BF16, device=DEV)
+    L.clha_fp4_matmul(ctx, f, xq, xs, rows, 128, wq, ws, 16512, y)
+    small = torch.empty((257, 16512), dtype=BF16, device=DEV)
+    L.clha_fp4_matmul(ctx, f, xq[-257:].contiguous(), xs[-3 * 512:].contiguous(), 257, 128, wq, ws, 16512, small)
+    assert torch.equal(y[-257:], small)
+    L.clha_check(ctx)
+    del codes, scales, y, small, xq
+    torch.cuda.empty_cache()

@@ -80,7 +80,7 @@ def test_combine_buffers():
         with pytest.raises(ValueError, match=next(iter(kw))):
             call(**kw)
     with pytest.raises(TypeError, match="add"):
-        call(add=t(4, 128, dtype=BF16))
+        call(add=t(4, 128, dtype=I32))
 
 
 def test_null_context(lib):
@@ -91,4 +91,4 @@ def test_null_context(lib):
     assert lib.clha_fp4_dequantize(n, n, n, 0, 128, 0, n, 0, n, 0) == L.ERR_INVALID_ARG
     assert lib.clha_fp4_matmul(n, 0, n, n, n, 0, 128, n, 1, n, n, n, 128, n, 0) == L.ERR_INVALID_ARG
     assert lib.clha_fp4_expert_act(n, 0, n, n, n, 0, 128, n, 1, n, n, n, n, n, n, 128, n) == L.ERR_INVALID_ARG
-    assert lib.clha_combine(n, n, 0, 0, 128, n, n, 0, 1, 1, n, n, n, n, 0) == L.ERR_INVALID_ARG
+    assert lib.clha_combine(n, n, 0, 0, 128, n, n, 0, 1, 1, n, n, n, 0, n, 0) == L.ERR_INVALID_ARG
