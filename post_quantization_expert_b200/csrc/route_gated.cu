@@ -10,8 +10,9 @@
 // token takes only as many lanes as give each 8 experts or more (4 lanes for 32 experts, 8 for 64, ... all 32
 // from 256 on; the lanes of a token hold consecutive experts), and a round is a float maximum over the
 // lane, log2(lanes) exchanges, a vote for the first lane that has it, and a scan of the winner's 8 values.
-// Groups fit this where a group is a power of two of whole lanes; other group sizes, more than 512 experts, and
-// k above twice the lanes take the general kernel (a warp a token, lane i holds experts i, i + 32, ...).
+// A group that is a power of two of whole lanes is ranked by its own lanes, others (up to 32 of them) one after
+// the other by all. More than 512 experts, more groups, and k above twice the lanes take the general kernel (a
+// warp a token, lane i holds experts i, i + 32, ...).
 // 32768 tokens x 64 experts, top 6: general kernel 44 us, this one 16 us (about 10 of them the two launches, the
 // counters' clearing and the kernel); 9973 x 256 in 8 groups, top 8, with a bias: general 87 us, this one 32 us
 // (23 us in float32 alone).
@@ -32,6 +33,7 @@ struct GateArgs {
     const void* logits;
     int64_t n;
     int E, k, sigmoid, n_groups, top_groups, top2, renorm;
+    int group_lanes;         // lanes kernel: whole lanes of a group, a power of two; 0: groups cut through lanes
     float scale;
     const float* bias;
     int32_t* ids;
@@ -503,21 +505,43 @@ __global__ void __launch_bounds__(kWarps * 32, VPL == 8 ? 4 : 2) route_lanes_ker
         }
         bool open = false;                                   // a decision inside the error bound
         if (p.n_groups > 1) {
-            const int q = p.E / p.n_groups / VPL;            // lanes a group, a power of two
-            float a = -INFINITY, b = -INFINITY;              // the two largest choices of the group
+            const int size = p.E / p.n_groups;
+            const int q = p.group_lanes ? p.group_lanes : 1; // lanes a group, a power of two; or lane h has group h's rank
+            float rank = -INFINITY;
+            if (p.group_lanes) {
+                float a = -INFINITY, b = -INFINITY;          // the two largest choices of the group
 #pragma unroll
-            for (int i = 0; i < VPL; ++i) {
-                b = fmaxf(b, fminf(a, c[i]));
-                a = fmaxf(a, c[i]);
+                for (int i = 0; i < VPL; ++i) {
+                    b = fmaxf(b, fminf(a, c[i]));
+                    a = fmaxf(a, c[i]);
+                }
+                for (int o = 1; o < q; o <<= 1) {
+                    const float oa = __shfl_xor_sync(kAll, a, o), ob = __shfl_xor_sync(kAll, b, o);
+                    b = fmaxf(fmaxf(b, ob), fminf(a, oa));
+                    a = fmaxf(a, oa);
+                }
+                if (e0 < p.E) rank = p.top2 ? a + b : a;
+            } else {
+                for (int h = 0; h < p.n_groups; ++h) {
+                    const unsigned from = h * size - e0;     // the group's first expert among this lane's
+                    float a = -INFINITY, b = -INFINITY;
+#pragma unroll
+                    for (int i = 0; i < VPL; ++i)
+                        if (i - from < (unsigned)size) {
+                            b = fmaxf(b, fminf(a, c[i]));
+                            a = fmaxf(a, c[i]);
+                        }
+#pragma unroll
+                    for (int o = LPT / 2; o; o >>= 1) {
+                        const float oa = __shfl_xor_sync(kAll, a, o), ob = __shfl_xor_sync(kAll, b, o);
+                        b = fmaxf(fmaxf(b, ob), fminf(a, oa));
+                        a = fmaxf(a, oa);
+                    }
+                    if (sub == h) rank = p.top2 && size > 1 ? a + b : a;
+                }
             }
-            for (int o = 1; o < q; o <<= 1) {
-                const float oa = __shfl_xor_sync(kAll, a, o), ob = __shfl_xor_sync(kAll, b, o);
-                b = fmaxf(fmaxf(b, ob), fminf(a, oa));
-                a = fmaxf(a, oa);
-            }
-            const bool in = e0 < p.E;
-            const float rank = !in ? -INFINITY : p.top2 ? a + b : a;
             const int g = sub / q;
+            const bool in = g < p.n_groups;
             int ahead = 0;
             for (int h = 0; h < p.n_groups; ++h) {
                 const float r = __shfl_sync(kAll, rank, first + h * q);
@@ -525,13 +549,23 @@ __global__ void __launch_bounds__(kWarps * 32, VPL == 8 ? 4 : 2) route_lanes_ker
             }
             const bool kept = in && ahead < p.top_groups;
             if (!by_logit && p.top_groups < p.n_groups) {    // the last kept and the first dropped rank
-                const float above = -lanes_max<LPT>(in && kept ? -rank : -INFINITY);
+                const float above = -lanes_max<LPT>(kept ? -rank : -INFINITY);
                 const float below = lanes_max<LPT>(in && !kept ? rank : -INFINITY);
                 open = above - below <= 3 * slack;
             }
-            if (!kept) {
+            const unsigned stay = __ballot_sync(kAll, kept) >> first;   // by lanes
+            if (p.group_lanes) {
+                if (!kept) {
 #pragma unroll
-                for (int i = 0; i < VPL; ++i) c[i] = -INFINITY;
+                    for (int i = 0; i < VPL; ++i) c[i] = -INFINITY;
+                }
+            } else {
+                int h = e0 / size, left = (h + 1) * size - e0;          // the expert's group; experts left in it
+#pragma unroll
+                for (int i = 0; i < VPL; ++i) {
+                    if (!(stay >> h & 1)) c[i] = -INFINITY;
+                    if (--left == 0) { ++h; left = size; }
+                }
             }
         }
         float last = INFINITY;
@@ -592,11 +626,13 @@ __global__ void __launch_bounds__(kWarps * 32, VPL == 8 ? 4 : 2) route_lanes_ker
 }
 
 template <typename T>
-cudaError_t launch_t(cudaStream_t s, int num_sms, const GateArgs& p) {
-    const int lpt = p.E <= 32 ? 4 : p.E <= 64 ? 8 : p.E <= 128 ? 16 : 32;
-    const int vpl = p.E <= 256 ? 8 : 16;
-    const int size = p.E / p.n_groups, q = size / vpl;
-    const bool lanes = p.E <= 512 && p.k <= 2 * lpt && (p.n_groups == 1 || (size % vpl == 0 && (q & (q - 1)) == 0));
+cudaError_t launch_t(cudaStream_t s, int num_sms, GateArgs p) {
+    const int vpl = p.E <= 256 ? 8 : 16, size = p.E / p.n_groups, q = size / vpl;
+    int lpt = p.E <= 32 ? 4 : p.E <= 64 ? 8 : p.E <= 128 ? 16 : 32;
+    p.group_lanes = size % vpl == 0 && (q & (q - 1)) == 0 ? q : 0;
+    if (!p.group_lanes)
+        while (lpt < 32 && lpt < p.n_groups) lpt *= 2;       // a lane for each group's rank
+    const bool lanes = p.E <= 512 && p.k <= 2 * lpt && (p.n_groups == 1 || p.group_lanes || p.n_groups <= lpt);
     const int tokens = kWarps * (lanes ? 32 / lpt : 1);      // a block's tokens at a time
     int64_t blocks = (p.n + tokens - 1) / tokens;
     // up to two rounds of one block: it overwrites the counts, and the clearing launch is saved
@@ -615,11 +651,11 @@ cudaError_t launch_t(cudaStream_t s, int num_sms, const GateArgs& p) {
         const int vec = p.E % 8 == 0 && ((uintptr_t)p.logits & 15) == 0;
 #define CLHA_GATE(L, V) \
     e = clha_launch_overlapped(route_lanes_kernel<T, L, V>, (unsigned)blocks, kWarps * 32, smem, s, 1, p, one, vec)
-        if (p.E <= 32) CLHA_GATE(4, 8);
-        else if (p.E <= 64) CLHA_GATE(8, 8);
-        else if (p.E <= 128) CLHA_GATE(16, 8);
-        else if (p.E <= 256) CLHA_GATE(32, 8);
-        else CLHA_GATE(32, 16);
+        if (vpl == 16) CLHA_GATE(32, 16);
+        else if (lpt == 4) CLHA_GATE(4, 8);
+        else if (lpt == 8) CLHA_GATE(8, 8);
+        else if (lpt == 16) CLHA_GATE(16, 8);
+        else CLHA_GATE(32, 8);
 #undef CLHA_GATE
     } else {
 #define CLHA_GATE(V) \
@@ -643,6 +679,6 @@ cudaError_t launch_route_gated(cudaStream_t s, int num_sms, const void* logits, 
                                const clha_route_params& rp, const float* bias, int32_t* ids, float* weights,
                                int32_t* counts, int* err) {
     GateArgs p{logits, n, rp.E, rp.k, rp.score == CLHA_SCORE_SIGMOID, rp.n_groups, rp.top_groups,
-               rp.group_rank == CLHA_GROUP_TOP2, rp.renormalise != 0, rp.scale, bias, ids, weights, counts, err};
+               rp.group_rank == CLHA_GROUP_TOP2, rp.renormalise != 0, 0, rp.scale, bias, ids, weights, counts, err};
     return is_f32 ? launch_t<float>(s, num_sms, p) : launch_t<__nv_bfloat16>(s, num_sms, p);
 }

@@ -351,7 +351,10 @@ def check_route(ctx, l, k, bias=None, **kw):
 @pytest.mark.parametrize("n,E,k,groups,top,rank", [
     (1, 1, 1, 1, 1, "max"), (3, 7, 7, 1, 1, "max"), (16, 64, 6, 1, 1, "max"), (17, 64, 6, 8, 3, "top2"),
     (200, 256, 8, 8, 4, "top2"), (33, 40, 4, 5, 2, "max"), (50, 96, 10, 48, 9, "top2"), (40, 12, 3, 12, 5, "top2"),
-    (9, 1024, 32, 1, 1, "max"), (9, 1000, 40, 40, 7, "top2"), (70, 300, 5, 3, 1, "max")])
+    (9, 1024, 32, 1, 1, "max"), (9, 1000, 40, 40, 7, "top2"), (70, 300, 5, 3, 1, "max"),
+    # groups that cut through a lane's experts, groups of one and of two experts, more groups than lanes for the experts
+    (300, 100, 7, 4, 2, "top2"), (61, 16, 4, 8, 3, "top2"), (61, 30, 4, 30, 6, "max"), (130, 328, 9, 8, 5, "top2"),
+    (45, 20, 2, 2, 1, "max"), (45, 510, 8, 30, 11, "top2"), (20, 512, 8, 2, 1, "top2"), (20, 384, 8, 4, 3, "max")])
 def test_route_gated(ctx, score, dtype, biased, n, E, k, groups, top, rank):
     l = torch.randn((n, E), generator=gen(n * E)).to(dtype)
     bias = 0.2 * torch.randn(E, generator=gen(E)) if biased else None
