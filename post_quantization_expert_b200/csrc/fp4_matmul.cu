@@ -592,7 +592,7 @@ fp4_matmul_pair_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_con
             tc::tmem_wait_ld();
             tc::fence_before_sync();
             __syncwarp();
-            if (lane == 0) tc::mbar_arrive_cluster(tempty_leader);
+            if (lane == 0) tc::mbar_arrive_cluster_relaxed(tempty_leader);
             const int col = nt * TILE_N + half * (ACT ? 64 : 128);
             if (r0 >= k.pend || col >= p.N) continue;  // rows of another segment; the missing half of an odd N
             constexpr int PER = 128 / (int)sizeof(OUT);                // columns of a 128-byte box
