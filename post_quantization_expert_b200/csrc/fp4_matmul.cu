@@ -443,7 +443,7 @@ fp4_matmul_pair_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_con
     volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
     const uint32_t rank = tc::cluster_ctarank();
     const bool leader = rank == 0;
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int warp = tc::warp_index(), lane = threadIdx.x & 31;
     const int64_t pair = blockIdx.x >> 1, npairs = gridDim.x >> 1;
     if (threadIdx.x == 0) {
         for (int s = 0; s < C::STAGES; ++s) {
@@ -508,62 +508,71 @@ fp4_matmul_pair_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_con
         }
         __syncwarp();
     } else if (warp == 1) {
-        if (lane == 0 && leader) {
+        if (leader) {
             constexpr uint32_t kE8 = BLOCK == 32;
             constexpr uint32_t ID0 = tc::idesc_fp4(kE8, 256, 256, 0), ID2 = tc::idesc_fp4(kE8, 256, 256, 2);
+            const bool issuer = tc::elect_one();
+            const uint64_t desc0 = tc::sw128_desc(tc::smem_u32(smem), 16, 1024);
             Walk k;
-            int it = 0, tcount = 0;
+            int s = 0, tcount = 0;
+            uint32_t ph = 0;
             bool ok = true;
             for (int64_t w = pair; ok && k.at(p, w); w += npairs, ++tcount) {
-                if (!tc::mbar_wait_bounded(tempty, (tcount & 1) ^ 1, abort_flag)) { ok = false; break; }
+                if (!tc::mbar_wait_warp(tempty, (tcount & 1) ^ 1, abort_flag)) { ok = false; break; }
                 tc::fence_after_sync();
-                for (int kb = 0; kb < nk; ++kb, ++it) {
-                    const int s = it % C::STAGES;
-                    const uint32_t ph = (it / C::STAGES) & 1;
-                    if (!tc::mbar_wait_bounded(full0 + 8 * s, ph, abort_flag) ||
-                        !tc::mbar_wait_bounded(sready0 + 8 * s, ph, abort_flag)) { ok = false; break; }
+                for (int kb = 0; kb < nk; ++kb) {
+                    // (the scale warps have waited for the stage's operands)
+                    if (!tc::mbar_wait_warp(sready0 + 8 * s, ph, abort_flag)) { ok = false; break; }
                     tc::fence_after_sync();
-                    const uint32_t a = tc::smem_u32(smem + s * C::STAGE_STRIDE);
-                    const uint32_t b = a + TILE_BYTES;
+                    const uint64_t ad = desc0 + (uint32_t)(s * (C::STAGE_STRIDE >> 4)), bd = ad + (TILE_BYTES >> 4);
                     const uint32_t ta = tmem + 256 + s * C::SF_COLS, tb = ta + C::APS * 4;
-                    const int steps = p.K - kb * 256 >= 256 ? 4 : 2;   // K is a multiple of 128
+                    const bool full_k = p.K - kb * 256 >= 256;         // else half: K is a multiple of 128
+                    if (issuer) {
 #pragma unroll
-                    for (int kk = 0; kk < 4; ++kk) {
-                        if (kk >= steps) break;
-                        const int j = BLOCK == 16 ? kk : kk >> 1;
-                        tc::mma_fp4_pair<BLOCK>(tmem, tc::sw128_desc(a + kk * 32, 16, 1024),
-                                                tc::sw128_desc(b + kk * 32, 16, 1024),
-                                                BLOCK == 32 && (kk & 1) ? ID2 : ID0, ta + 4 * j, tb + 8 * j, (kb | kk) != 0);
+                        for (int kk = 0; kk < 4; ++kk) {
+                            if (kk >= 2 && !full_k) break;
+                            const int j = BLOCK == 16 ? kk : kk >> 1;
+                            tc::mma_fp4_pair<BLOCK>(tmem, ad + 2 * kk, bd + 2 * kk, BLOCK == 32 && (kk & 1) ? ID2 : ID0,
+                                                    ta + 4 * j, tb + 8 * j, kk != 0 || kb != 0);
+                        }
+                        tc::mma_commit_pair(empty0 + 8 * s, 0x3);
+                        if (kb == nk - 1) tc::mma_commit_pair(tfull, 0x3);
                     }
-                    tc::mma_commit_pair(empty0 + 8 * s, 0x3);
+                    __syncwarp();
+                    if (++s == C::STAGES) { s = 0; ph ^= 1; }
                 }
-                if (ok) tc::mma_commit_pair(tfull, 0x3);
             }
         }
         __syncwarp();
     } else if (warp >= 10) {
-        if (lane == 0 && leader) {
+        if (leader) {
+            const bool issuer = tc::elect_one();
+            const uint64_t desc0 = tc::plain_desc(tc::smem_u32(smem) + 2 * TILE_BYTES);
             Walk k;
-            int it = 0;
+            int s = 0;
+            uint32_t ph = 0;
             bool ok = true;
             for (int64_t w = pair; ok && k.at(p, w); w += npairs)
-                for (int kb = 0; kb < nk; ++kb, ++it) {
-                    const int s = it % C::STAGES;
-                    if (!tc::mbar_wait_bounded(full0 + 8 * s, (it / C::STAGES) & 1, abort_flag)) { ok = false; break; }
+                for (int kb = 0; kb < nk; ++kb) {
+                    if (!tc::mbar_wait_warp(full0 + 8 * s, ph, abort_flag)) { ok = false; break; }
                     tc::fence_after_sync();
-                    const uint32_t sf = tc::smem_u32(smem + s * C::STAGE_STRIDE) + 2 * TILE_BYTES;
+                    const uint64_t sd = desc0 + (uint32_t)(s * (C::STAGE_STRIDE >> 4));
                     const uint32_t ta = tmem + 256 + s * C::SF_COLS, tb = ta + C::APS * 4;
+                    if (issuer) {
 #pragma unroll
-                    for (int j = 0; j < C::APS; ++j) {
-                        if ((j & 1) != warp - 10) continue;
-                        tc::tmem_copy_scales_pair(ta + 4 * j, tc::plain_desc(sf + j * 512));
-                        tc::tmem_copy_scales_pair(tb + 8 * j, tc::plain_desc(sf + C::SF_BYTES + j * 512));
-                        tc::tmem_copy_scales_pair(tb + 8 * j + 4, tc::plain_desc(sf + 2 * C::SF_BYTES + j * 512));
+                        for (int jj = 0; jj < C::APS / 2; ++jj) {
+                            const int j = 2 * jj + (warp - 10);
+                            tc::tmem_copy_scales_pair(ta + 4 * j, sd + j * 32);
+                            tc::tmem_copy_scales_pair(tb + 8 * j, sd + (C::SF_BYTES >> 4) + j * 32);
+                            tc::tmem_copy_scales_pair(tb + 8 * j + 4, sd + (C::SF_BYTES >> 3) + j * 32);
+                        }
+                        tc::mma_commit_pair(sready0 + 8 * s, 0x1);
                     }
-                    tc::mma_commit_pair(sready0 + 8 * s, 0x1);
+                    __syncwarp();
+                    if (++s == C::STAGES) { s = 0; ph ^= 1; }
                 }
             // the copies that this thread issued are done before the CTA gives its TMEM back
-            tc::mma_commit_pair(drain, 0x1);
+            if (issuer) tc::mma_commit_pair(drain, 0x1);
         }
         __syncwarp();
     } else {
@@ -639,7 +648,7 @@ fp4_matmul_pair_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_con
 
     __syncthreads();
     if (warp == 1 && leader) {
-        if (lane == 0) {
+        if (tc::elect_one()) {                     // (the lane that issued the products)
             tc::mma_commit_pair(drain, 0x1);
             tc::mbar_wait_bounded(drain, 0, abort_flag, 100000000ull);
         }
