@@ -119,7 +119,7 @@ fp4_matmul_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant
     const uint32_t drain = tempty0 + 8 * C::ACCS;
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 3 * C::STAGES + 2 * C::ACCS + 1);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int warp = tc::warp_index(), lane = threadIdx.x & 31;
     const int S = p.split;
     const int rank = S > 1 ? (int)tc::cluster_ctarank() : 0;
 
@@ -210,63 +210,70 @@ fp4_matmul_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant
         }
         __syncwarp();
     } else if (warp == 1) {
-        if (lane == 0) {
-            int it = 0, tcount = 0;
-            bool ok = true;
-            for (int64_t w = w0; ok && w < total; w += stride, ++tcount) {
-                const Tile t = tile(w);
-                const uint32_t n16 = max(1, (t.tokens + 15) / 16);
-                const uint32_t id0 = tc::idesc_fp4(BLOCK == 32, 128, n16 * 16, 0);
-                const uint32_t id2 = tc::idesc_fp4(BLOCK == 32, 128, n16 * 16, 2);
-                const int acc = tcount % C::ACCS;
-                if (!tc::mbar_wait_bounded(tempty0 + 8 * acc, ((tcount / C::ACCS) & 1) ^ 1, abort_flag)) { ok = false; break; }
+        const bool issuer = tc::elect_one();
+        const uint64_t desc0 = tc::sw128_desc(tc::smem_u32(smem), 16, 1024);
+        int s = 0, tcount = 0;
+        uint32_t ph = 0;
+        bool ok = true;
+        for (int64_t w = w0; ok && w < total; w += stride, ++tcount) {
+            const Tile t = tile(w);
+            const uint32_t n16 = max(1, (t.tokens + 15) / 16);
+            const uint32_t id0 = tc::idesc_fp4(BLOCK == 32, 128, n16 * 16, 0);
+            const uint32_t id2 = tc::idesc_fp4(BLOCK == 32, 128, n16 * 16, 2);
+            const int acc = tcount % C::ACCS;
+            if (!tc::mbar_wait_warp(tempty0 + 8 * acc, ((tcount / C::ACCS) & 1) ^ 1, abort_flag)) { ok = false; break; }
+            tc::fence_after_sync();
+            const uint32_t d_tmem = tmem + acc * (NB * XR);
+            for (int kb = k_lo; kb < k_hi; ++kb) {
+                // (the scale warps have waited for the stage's operands)
+                if (!tc::mbar_wait_warp(sready0 + 8 * s, ph, abort_flag)) { ok = false; break; }
                 tc::fence_after_sync();
-                const uint32_t d_tmem = tmem + acc * (NB * XR);
-                for (int kb = k_lo; kb < k_hi; ++kb, ++it) {
-                    const int s = it % C::STAGES;
-                    const uint32_t ph = (it / C::STAGES) & 1;
-                    if (!tc::mbar_wait_bounded(full0 + 8 * s, ph, abort_flag) ||
-                        !tc::mbar_wait_bounded(sready0 + 8 * s, ph, abort_flag)) { ok = false; break; }
-                    tc::fence_after_sync();
-                    const uint32_t a = tc::smem_u32(smem + s * C::STAGE_BYTES);
-                    const uint32_t b = a + NB * TILE_BYTES;
-                    const uint32_t tw = tmem + C::SF_BASE + s * C::SF_COLS, tx = tw + NB * C::APS * 4;
-                    const int steps = p.K - kb * 256 >= 256 ? 4 : 2;   // K is a multiple of 128
+                const uint64_t ad = desc0 + (uint32_t)(s * (C::STAGE_BYTES >> 4)), xd = ad + (NB * TILE_BYTES >> 4);
+                const uint32_t tw = tmem + C::SF_BASE + s * C::SF_COLS, tx = tw + NB * C::APS * 4;
+                const bool full_k = p.K - kb * 256 >= 256;             // else half: K is a multiple of 128
+                if (issuer) {
 #pragma unroll
                     for (int kk = 0; kk < 4; ++kk) {
-                        if (kk >= steps) break;
+                        if (kk >= 2 && !full_k) break;
                         const int j = BLOCK == 16 ? kk : kk >> 1;
-                        const uint32_t id = BLOCK == 32 && (kk & 1) ? id2 : id0;
-                        const uint64_t xd = tc::sw128_desc(b + kk * 32, 16, 1024);
 #pragma unroll
                         for (int x = 0; x < NB; ++x)
-                            tc::mma_fp4<BLOCK>(d_tmem + x * XR, tc::sw128_desc(a + x * TILE_BYTES + kk * 32, 16, 1024), xd, id,
-                                               tw + 4 * (x * C::APS + j), tx + 4 * j, kb != k_lo || kk != 0);
+                            tc::mma_fp4<BLOCK>(d_tmem + x * XR, ad + (x * (TILE_BYTES >> 4) + 2 * kk), xd + 2 * kk,
+                                               BLOCK == 32 && (kk & 1) ? id2 : id0, tw + 4 * (x * C::APS + j), tx + 4 * j,
+                                               kb != k_lo || kk != 0);
                     }
                     tc::mma_commit(empty0 + 8 * s);
+                    if (kb == k_hi - 1) tc::mma_commit(tfull0 + 8 * acc);
                 }
-                if (ok) tc::mma_commit(tfull0 + 8 * acc);
+                __syncwarp();
+                if (++s == C::STAGES) { s = 0; ph ^= 1; }
             }
         }
         __syncwarp();
     } else if (warp >= 10) {
-        if (lane == 0) {
-            int it = 0;
-            bool ok = true;
-            for (int64_t w = w0; ok && w < total; w += stride)
-                for (int kb = k_lo; kb < k_hi; ++kb, ++it) {
-                    const int s = it % C::STAGES;
-                    if (!tc::mbar_wait_bounded(full0 + 8 * s, (it / C::STAGES) & 1, abort_flag)) { ok = false; break; }
-                    tc::fence_after_sync();
-                    const uint32_t sf = tc::smem_u32(smem + s * C::STAGE_BYTES) + NB * TILE_BYTES + XR * BKB;
-                    const uint32_t ts = tmem + C::SF_BASE + s * C::SF_COLS;
+        const bool issuer = tc::elect_one();
+        const uint64_t desc0 = tc::plain_desc(tc::smem_u32(smem) + NB * TILE_BYTES + XR * BKB);
+        int s = 0;
+        uint32_t ph = 0;
+        bool ok = true;
+        for (int64_t w = w0; ok && w < total; w += stride)
+            for (int kb = k_lo; kb < k_hi; ++kb) {
+                if (!tc::mbar_wait_warp(full0 + 8 * s, ph, abort_flag)) { ok = false; break; }
+                tc::fence_after_sync();
+                const uint64_t sd = desc0 + (uint32_t)(s * (C::STAGE_BYTES >> 4));
+                const uint32_t ts = tmem + C::SF_BASE + s * C::SF_COLS;
+                if (issuer) {
 #pragma unroll
-                    for (int j = 0; j < (NB + 1) * C::APS; ++j)
-                        if ((j & 1) == warp - 10) tc::tmem_copy_scales(ts + 4 * j, tc::plain_desc(sf + j * 512));
+                    for (int jj = 0; jj < (NB + 1) * C::APS / 2; ++jj) {
+                        const int j = 2 * jj + (warp - 10);
+                        tc::tmem_copy_scales(ts + 4 * j, sd + j * 32);
+                    }
                     tc::mma_commit(sready0 + 8 * s);
                 }
-            tc::mma_commit(drain);   // the copies that this thread issued are done before the CTA gives its TMEM back
-        }
+                __syncwarp();
+                if (++s == C::STAGES) { s = 0; ph ^= 1; }
+            }
+        if (issuer) tc::mma_commit(drain);   // the copies that this thread issued are done before the CTA gives its TMEM back
         __syncwarp();
     } else {
         const int q = warp & 3, half = (warp - 2) >> 2;
@@ -355,7 +362,7 @@ fp4_matmul_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant
         __syncthreads();
     }
     if (warp == 1) {
-        if (lane == 0) {
+        if (tc::elect_one()) {                     // (the lane that issued the products)
             tc::mma_commit(drain);
             tc::mbar_wait_bounded(drain, 0, abort_flag, 100000000ull);
         }
