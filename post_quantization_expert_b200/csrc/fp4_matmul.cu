@@ -12,10 +12,13 @@
 // and more of shared memory is left for W's copies in flight.
 //   warp 0       TMA producer: per 256 columns of K, 128 bytes a row of W and of X (128-byte swizzle) and
 //                their scale tiles (512 bytes for 128 rows x 4 blocks, copied as they lie).
-//   warp 1       issues the products of 64 columns of K each.
+//   warp 1       copies the stage's scale tiles to TMEM (its own columns for each stage, so that the stage's
+//                barriers also order their reuse) and issues the products of 64 columns of K each.
 //   warps 2-9    epilogue: two warps for each TMEM lane quadrant (32 columns of Y), rows in turns.
-//   warps 10, 11 copy the stage's scale tiles to TMEM, every other one each (its own TMEM columns for each
-//                stage, so that the stage's barriers also order their reuse).
+// Warp 1 runs its loop as a whole and one elected lane issues: its instructions' operands are then uniform
+// registers. Issued under `if (lane == 0)`, a stage of the large tiles took 730 cycles to issue, whatever the
+// products' size, and a scale copy about 60, so that extra warps for the copies paid (28672 -> 8192 on 16384
+// tokens: 2.35 ms, 1.73 ms with two warps for the copies, 1.58 ms issued this way, with or without those warps).
 // With few tiles, `split` CTAs of a cluster share one tile's K range and add their parts through distributed
 // shared memory, in rank order, so that the result does not depend on timing.
 #include "clha_internal.h"
@@ -24,7 +27,7 @@
 
 namespace {
 
-constexpr int kThreads = 384;
+constexpr int kThreads = 320;
 constexpr int BKB = 128;                        // bytes of K a stage (256 columns)
 constexpr int TILE_BYTES = 128 * BKB;           // 16 KB: 128 rows of a stage
 constexpr int MAX_SMEM = 232448;
@@ -47,7 +50,7 @@ struct Cfg {
     static constexpr int STAGES = FIT < TFIT ? FIT : TFIT;
     static constexpr int SEG_OFF = STAGES * STAGE_BYTES;
     static constexpr int BAR_OFF = SEG_OFF + SEG_BYTES;
-    static constexpr int SMEM = BAR_OFF + 8 * (3 * STAGES + 2 * ACCS + 1) + 16 + 1024;
+    static constexpr int SMEM = BAR_OFF + 8 * (2 * STAGES + 2 * ACCS + 1) + 16 + 1024;
     static_assert((SMEM + 1024) * CTAS <= MAX_SMEM + 1024 && STAGES >= 4, "shared memory");
     static_assert(STAGE_BYTES % 1024 == 0 && BAR_OFF % 8 == 0, "alignment");
     static_assert(STAGES * STAGE_BYTES >= NB * XR * 128 * 4, "partial sums fit the stages");
@@ -113,11 +116,10 @@ fp4_matmul_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant
     uint64_t* bars = reinterpret_cast<uint64_t*>(smem + C::BAR_OFF);
     const uint32_t full0 = tc::smem_u32(bars);
     const uint32_t empty0 = full0 + 8 * C::STAGES;
-    const uint32_t sready0 = empty0 + 8 * C::STAGES;      // a stage's scales are on their way to TMEM
-    const uint32_t tfull0 = sready0 + 8 * C::STAGES;      // accumulator a holds a finished tile
+    const uint32_t tfull0 = empty0 + 8 * C::STAGES;      // accumulator a holds a finished tile
     const uint32_t tempty0 = tfull0 + 8 * C::ACCS;        // accumulator a has been read
     const uint32_t drain = tempty0 + 8 * C::ACCS;
-    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 3 * C::STAGES + 2 * C::ACCS + 1);
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 2 * C::STAGES + 2 * C::ACCS + 1);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
     const int warp = tc::warp_index(), lane = threadIdx.x & 31;
     const int S = p.split;
@@ -127,13 +129,12 @@ fp4_matmul_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant
         for (int s = 0; s < C::STAGES; ++s) {
             tc::mbar_init(full0 + 8 * s, 1);
             tc::mbar_init(empty0 + 8 * s, 1);
-            tc::mbar_init(sready0 + 8 * s, 2);            // one arrival per scale warp
         }
         for (int a = 0; a < C::ACCS; ++a) {
             tc::mbar_init(tfull0 + 8 * a, 1);
             tc::mbar_init(tempty0 + 8 * a, 8);            // one arrival per epilogue warp
         }
-        tc::mbar_init(drain, 3);                          // the products' thread and the scale warps
+        tc::mbar_init(drain, 1);
         *abort_flag = 0;
         tc::fence_barrier_init();
         tc::prefetch_tmap(&tmX);
@@ -212,6 +213,7 @@ fp4_matmul_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant
     } else if (warp == 1) {
         const bool issuer = tc::elect_one();
         const uint64_t desc0 = tc::sw128_desc(tc::smem_u32(smem), 16, 1024);
+        const uint64_t sdesc0 = tc::plain_desc(tc::smem_u32(smem) + NB * TILE_BYTES + XR * BKB);
         int s = 0, tcount = 0;
         uint32_t ph = 0;
         bool ok = true;
@@ -225,13 +227,15 @@ fp4_matmul_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant
             tc::fence_after_sync();
             const uint32_t d_tmem = tmem + acc * (NB * XR);
             for (int kb = k_lo; kb < k_hi; ++kb) {
-                // (the scale warps have waited for the stage's operands)
-                if (!tc::mbar_wait_warp(sready0 + 8 * s, ph, abort_flag)) { ok = false; break; }
+                if (!tc::mbar_wait_warp(full0 + 8 * s, ph, abort_flag)) { ok = false; break; }
                 tc::fence_after_sync();
                 const uint64_t ad = desc0 + (uint32_t)(s * (C::STAGE_BYTES >> 4)), xd = ad + (NB * TILE_BYTES >> 4);
                 const uint32_t tw = tmem + C::SF_BASE + s * C::SF_COLS, tx = tw + NB * C::APS * 4;
+                const uint64_t sd = sdesc0 + (uint32_t)(s * (C::STAGE_BYTES >> 4));
                 const bool full_k = p.K - kb * 256 >= 256;             // else half: K is a multiple of 128
                 if (issuer) {
+#pragma unroll
+                    for (int j = 0; j < (NB + 1) * C::APS; ++j) tc::tmem_copy_scales(tw + 4 * j, sd + j * 32);
 #pragma unroll
                     for (int kk = 0; kk < 4; ++kk) {
                         if (kk >= 2 && !full_k) break;
@@ -249,31 +253,6 @@ fp4_matmul_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant
                 if (++s == C::STAGES) { s = 0; ph ^= 1; }
             }
         }
-        __syncwarp();
-    } else if (warp >= 10) {
-        const bool issuer = tc::elect_one();
-        const uint64_t desc0 = tc::plain_desc(tc::smem_u32(smem) + NB * TILE_BYTES + XR * BKB);
-        int s = 0;
-        uint32_t ph = 0;
-        bool ok = true;
-        for (int64_t w = w0; ok && w < total; w += stride)
-            for (int kb = k_lo; kb < k_hi; ++kb) {
-                if (!tc::mbar_wait_warp(full0 + 8 * s, ph, abort_flag)) { ok = false; break; }
-                tc::fence_after_sync();
-                const uint64_t sd = desc0 + (uint32_t)(s * (C::STAGE_BYTES >> 4));
-                const uint32_t ts = tmem + C::SF_BASE + s * C::SF_COLS;
-                if (issuer) {
-#pragma unroll
-                    for (int jj = 0; jj < (NB + 1) * C::APS / 2; ++jj) {
-                        const int j = 2 * jj + (warp - 10);
-                        tc::tmem_copy_scales(ts + 4 * j, sd + j * 32);
-                    }
-                    tc::mma_commit(sready0 + 8 * s);
-                }
-                __syncwarp();
-                if (++s == C::STAGES) { s = 0; ph ^= 1; }
-            }
-        if (issuer) tc::mma_commit(drain);   // the copies that this thread issued are done before the CTA gives its TMEM back
         __syncwarp();
     } else {
         const int q = warp & 3, half = (warp - 2) >> 2;
@@ -383,11 +362,7 @@ fp4_matmul_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant
 // through shared memory by TMA (boxes of 32 rows x 128 bytes), which cuts off rows behind the end of Y.
 // Tiles of an expert are taken in bands of 8 row tiles, rows fastest, so that the pairs working at one time
 // share about 8 row blocks and as many column blocks of L2.
-//
-// Two warps of their own copy the scales to TMEM, every other scale column each. Such a copy takes about 60
-// cycles in its issuer's order, and a stage of e4m3 scales has twelve: issued by the products' thread they ran
-// in line with its products (measured on 4096 x 16384 -> 9472: 441 us; from one other warp 343, from two 274;
-// without any copy 253). Writing the scales with tcgen05.st from registers took 547.
+// (Writing the scales from registers, with tcgen05.st from four warps, took twice the time of the copies.)
 template <int BLOCK>
 struct PairCfg {
     static constexpr int APS = 256 / BLOCK / 4;
@@ -398,7 +373,7 @@ struct PairCfg {
     static constexpr int STG_OFF = STAGES * ((STAGE_BYTES + 1023) / 1024 * 1024);
     static constexpr int STAGE_STRIDE = (STAGE_BYTES + 1023) / 1024 * 1024;
     static constexpr int BAR_OFF = STG_OFF + 8 * 4096;
-    static constexpr int SMEM = BAR_OFF + 8 * (3 * STAGES + 3) + 16 + 1024;
+    static constexpr int SMEM = BAR_OFF + 8 * (2 * STAGES + 3) + 16 + 1024;
     static_assert(SMEM <= MAX_SMEM, "shared memory");
     static_assert(256 + STAGES * SF_COLS <= 512, "tensor memory");
 };
@@ -445,8 +420,7 @@ fp4_matmul_pair_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_con
     const uint32_t tfull = empty0 + 8 * C::STAGES;        // each CTA: the accumulator holds a finished tile
     const uint32_t tempty = tfull + 8;                    // leader: both CTAs' epilogues have read it
     const uint32_t drain = tempty + 8;
-    const uint32_t sready0 = drain + 8;                   // leader: a stage's scales are on their way to TMEM
-    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 3 * C::STAGES + 3);
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 2 * C::STAGES + 3);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
     const uint32_t rank = tc::cluster_ctarank();
     const bool leader = rank == 0;
@@ -456,11 +430,10 @@ fp4_matmul_pair_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_con
         for (int s = 0; s < C::STAGES; ++s) {
             tc::mbar_init(full0 + 8 * s, 1);
             tc::mbar_init(empty0 + 8 * s, 1);
-            tc::mbar_init(sready0 + 8 * s, 2);            // one arrival per scale warp
         }
         tc::mbar_init(tfull, 1);
         tc::mbar_init(tempty, 16);                        // one arrival per epilogue warp of either CTA
-        tc::mbar_init(drain, 3);                          // the products' thread and the scale warps
+        tc::mbar_init(drain, 1);
         *abort_flag = 0;
         tc::fence_barrier_init();
     }
@@ -520,6 +493,7 @@ fp4_matmul_pair_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_con
             constexpr uint32_t ID0 = tc::idesc_fp4(kE8, 256, 256, 0), ID2 = tc::idesc_fp4(kE8, 256, 256, 2);
             const bool issuer = tc::elect_one();
             const uint64_t desc0 = tc::sw128_desc(tc::smem_u32(smem), 16, 1024);
+            const uint64_t sdesc0 = tc::plain_desc(tc::smem_u32(smem) + 2 * TILE_BYTES);
             Walk k;
             int s = 0, tcount = 0;
             uint32_t ph = 0;
@@ -528,13 +502,19 @@ fp4_matmul_pair_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_con
                 if (!tc::mbar_wait_warp(tempty, (tcount & 1) ^ 1, abort_flag)) { ok = false; break; }
                 tc::fence_after_sync();
                 for (int kb = 0; kb < nk; ++kb) {
-                    // (the scale warps have waited for the stage's operands)
-                    if (!tc::mbar_wait_warp(sready0 + 8 * s, ph, abort_flag)) { ok = false; break; }
+                    if (!tc::mbar_wait_warp(full0 + 8 * s, ph, abort_flag)) { ok = false; break; }
                     tc::fence_after_sync();
                     const uint64_t ad = desc0 + (uint32_t)(s * (C::STAGE_STRIDE >> 4)), bd = ad + (TILE_BYTES >> 4);
                     const uint32_t ta = tmem + 256 + s * C::SF_COLS, tb = ta + C::APS * 4;
+                    const uint64_t sd = sdesc0 + (uint32_t)(s * (C::STAGE_STRIDE >> 4));
                     const bool full_k = p.K - kb * 256 >= 256;         // else half: K is a multiple of 128
                     if (issuer) {
+#pragma unroll
+                        for (int j = 0; j < C::APS; ++j) {
+                            tc::tmem_copy_scales_pair(ta + 4 * j, sd + j * 32);
+                            tc::tmem_copy_scales_pair(tb + 8 * j, sd + (C::SF_BYTES >> 4) + j * 32);
+                            tc::tmem_copy_scales_pair(tb + 8 * j + 4, sd + (C::SF_BYTES >> 3) + j * 32);
+                        }
 #pragma unroll
                         for (int kk = 0; kk < 4; ++kk) {
                             if (kk >= 2 && !full_k) break;
@@ -549,37 +529,6 @@ fp4_matmul_pair_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_con
                     if (++s == C::STAGES) { s = 0; ph ^= 1; }
                 }
             }
-        }
-        __syncwarp();
-    } else if (warp >= 10) {
-        if (leader) {
-            const bool issuer = tc::elect_one();
-            const uint64_t desc0 = tc::plain_desc(tc::smem_u32(smem) + 2 * TILE_BYTES);
-            Walk k;
-            int s = 0;
-            uint32_t ph = 0;
-            bool ok = true;
-            for (int64_t w = pair; ok && k.at(p, w); w += npairs)
-                for (int kb = 0; kb < nk; ++kb) {
-                    if (!tc::mbar_wait_warp(full0 + 8 * s, ph, abort_flag)) { ok = false; break; }
-                    tc::fence_after_sync();
-                    const uint64_t sd = desc0 + (uint32_t)(s * (C::STAGE_STRIDE >> 4));
-                    const uint32_t ta = tmem + 256 + s * C::SF_COLS, tb = ta + C::APS * 4;
-                    if (issuer) {
-#pragma unroll
-                        for (int jj = 0; jj < C::APS / 2; ++jj) {
-                            const int j = 2 * jj + (warp - 10);
-                            tc::tmem_copy_scales_pair(ta + 4 * j, sd + j * 32);
-                            tc::tmem_copy_scales_pair(tb + 8 * j, sd + (C::SF_BYTES >> 4) + j * 32);
-                            tc::tmem_copy_scales_pair(tb + 8 * j + 4, sd + (C::SF_BYTES >> 3) + j * 32);
-                        }
-                        tc::mma_commit_pair(sready0 + 8 * s, 0x1);
-                    }
-                    __syncwarp();
-                    if (++s == C::STAGES) { s = 0; ph ^= 1; }
-                }
-            // the copies that this thread issued are done before the CTA gives its TMEM back
-            if (issuer) tc::mma_commit_pair(drain, 0x1);
         }
         __syncwarp();
     } else {
