@@ -9,6 +9,9 @@ This module only orders calls and owns device buffers; every step runs in libclh
   quantization clha_factor -> clha_quantize (gate, up share a factor) -> clha_loss
 Always-active shared experts see every token: their gate/up input Hessian is one slot shared by
 all of them, and they are quantized with one more bit (CLHA-MP).
+Fp4Layer runs a layer whose experts are in microscaled 4-bit floating point:
+  clha_route_gated -> clha_gather (permutation) -> clha_fp4_quantize -> clha_fp4_expert_act -> clha_fp4_quantize
+  -> clha_fp4_matmul -> clha_combine
 """
 from __future__ import annotations
 
