@@ -121,6 +121,7 @@ fp4_matmul_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant
     const uint32_t drain = tempty0 + 8 * C::ACCS;
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 2 * C::STAGES + 2 * C::ACCS + 1);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+    volatile int no_abort = 0;                             // for the waits after an abort
     const int warp = tc::warp_index(), lane = threadIdx.x & 31;
     const int S = p.split;
     const int rank = S > 1 ? (int)tc::cluster_ctarank() : 0;
@@ -179,9 +180,10 @@ fp4_matmul_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant
         return t;
     };
 
+    int issued = 0;                                        // producer: stages asked for
     if (warp == 0) {
         if (lane == 0) {
-            int it = 0;
+            int& it = issued;
             bool ok = true;
             for (int64_t w = w0; ok && w < total; w += stride) {
                 const Tile t = tile(w);
@@ -203,10 +205,6 @@ fp4_matmul_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant
                     tc::tma_load_2d(sf + NB * C::SF_BYTES, &tmXs, fb, 0, (int)(t.m0 / 128) * atoms + kb * C::APS);
                     for (int x = 0; x < boxes; ++x) tc::tma_load_2d(b + x * 16 * BKB, &tmX, fb, kb * BKB, (int)t.m0 + 16 * x);
                 }
-            }
-            if (!ok) {  // the copies already issued land before the CTA exits
-                for (int j = it - 1; j >= 0 && j >= it - C::STAGES; --j)
-                    tc::mbar_wait_bounded(full0 + 8 * (j % C::STAGES), (j / C::STAGES) & 1, abort_flag, 100000000ull);
             }
         }
         __syncwarp();
@@ -340,6 +338,10 @@ fp4_matmul_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant
     } else {
         __syncthreads();
     }
+    if (*abort_flag && warp == 0 && lane == 0)             // the copies asked for land before the CTA ends
+        for (int j = max(0, issued - C::STAGES); j < issued; ++j)
+            tc::mbar_wait_bounded(full0 + 8 * (j % C::STAGES), (j / C::STAGES) & 1, &no_abort, 100000000ull);
+    __syncwarp();
     if (warp == 1) {
         if (tc::elect_one()) {                     // (the lane that issued the products)
             tc::mma_commit(drain);
@@ -422,6 +424,7 @@ fp4_matmul_pair_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_con
     const uint32_t drain = tempty + 8;
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 2 * C::STAGES + 3);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+    volatile int no_abort = 0;                             // for the waits after an abort
     const uint32_t rank = tc::cluster_ctarank();
     const bool leader = rank == 0;
     const int warp = tc::warp_index(), lane = threadIdx.x & 31;
@@ -448,6 +451,7 @@ fp4_matmul_pair_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_con
     const int nk = (p.K + 255) / 256;
     const int atoms = p.K / BLOCK / 4;
 
+    int issued = 0;                                        // producer: stages asked for
     if (warp == 0) {
         if (lane == 0) {
             tc::prefetch_tmap(&tmX);
@@ -457,7 +461,7 @@ fp4_matmul_pair_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_con
             const uint32_t full_leader = tc::mapa_shared(full0, 0);
             const CUtensorMap* mb = ACT && rank ? &tmU : &tmW;      // this CTA's block of W
             Walk k;
-            int it = 0;
+            int& it = issued;
             bool ok = true;
             for (int64_t w = pair; ok && k.at(p, w); w += npairs) {
                 int64_t m0;
@@ -480,10 +484,6 @@ fp4_matmul_pair_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_con
                     tc::tma_load_2d_pair(sf + C::SF_BYTES, &tmWs, fb, 0, s0 + kb * C::APS);
                     tc::tma_load_2d_pair(sf + 2 * C::SF_BYTES, ACT ? &tmUs : &tmWs, fb, 0, s1 + kb * C::APS);
                 }
-            }
-            if (!ok && leader) {  // the copies already issued (both CTAs') land before either CTA can exit
-                for (int j = it - 1; j >= 0 && j >= it - C::STAGES; --j)
-                    tc::mbar_wait_bounded(full0 + 8 * (j % C::STAGES), (j / C::STAGES) & 1, abort_flag, 100000000ull);
             }
         }
         __syncwarp();
@@ -603,6 +603,10 @@ fp4_matmul_pair_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_con
     }
 
     __syncthreads();
+    if (*abort_flag && leader && warp == 0 && lane == 0)   // both CTAs' copies land before either CTA can end
+        for (int j = max(0, issued - C::STAGES); j < issued; ++j)
+            tc::mbar_wait_bounded(full0 + 8 * (j % C::STAGES), (j / C::STAGES) & 1, &no_abort, 100000000ull);
+    __syncwarp();
     if (warp == 1 && leader) {
         if (tc::elect_one()) {                     // (the lane that issued the products)
             tc::mma_commit_pair(drain, 0x1);

@@ -642,9 +642,13 @@ class Fp4Layer:
 
     def __init__(self, ctx: L.Context, w: MoEWeights, k: int, max_tokens: int, fmt: int = L.FP4_E4M3_16,
                  score: int = L.SCORE_SOFTMAX, bias: torch.Tensor | None = None, n_groups: int = 1, top_groups: int = 1,
-                 group_rank: int = L.GROUP_MAX, renormalise: bool = True, scale: float = 1.0, timer=NO_TIMER):
-        """w: the layer's weights (bf16 or f32). bias, n_groups, ... scale: as clha_route_gated takes them."""
+                 group_rank: int = L.GROUP_MAX, renormalise: bool = True, scale: float = 1.0,
+                 x_scale: torch.Tensor | None = None, h_scale: torch.Tensor | None = None, timer=NO_TIMER):
+        """w: the layer's weights (bf16 or f32). bias, n_groups, ... scale: as clha_route_gated takes them. x_scale,
+        h_scale (float32 [1] on the device): matrix scales of the layer's input and of the experts' activations, for
+        values that e4m3 block scales alone do not reach (above 2688, or around 2^-9 and below); none by default."""
         self.ctx, self.k, self.fmt, self.timer, self.max_tokens = ctx, k, fmt, timer, max_tokens
+        self.x_scale, self.h_scale = x_scale, h_scale
         self.E, self.d_model, self.d_ff = w.Wd.shape
         self.gate = dict(score=score, bias=bias, n_groups=n_groups, top_groups=top_groups, group_rank=group_rank,
                          renormalise=renormalise, scale=scale)
@@ -696,30 +700,31 @@ class Fp4Layer:
         if n > self.max_tokens:
             raise ValueError(f"{n} tokens in a layer built for {self.max_tokens}")
         P = L.clha_packed_rows(n, k, E)
-        dm, dff = self.d_model, self.d_ff
+        dm, dff, xs, hs = self.d_model, self.d_ff, self.x_scale, self.h_scale
         ids, weights = self.ids[:n], self.weights[:n]
         with t.span("route"):
             L.clha_route_gated(ctx, logits, n, E, k, ids, weights, self.counts, **self.gate)
             L.clha_gather(ctx, X, n, dm, ids, k, E, None, P, self.seg, self.perm)
         seg = dict(seg=self.seg, E=E)
         with t.span("quantize"):
-            L.clha_fp4_quantize(ctx, X, n, dm, fmt, *self.x, perm=self.perm, rows=P, **seg)
+            L.clha_fp4_quantize(ctx, X, n, dm, fmt, *self.x, tensor_scale=xs, perm=self.perm, rows=P, **seg)
         (g, gs, gg), (u, us, gu), (d, ds, gd) = *self.gate_up, self.down
         with t.span("act"):
-            L.clha_fp4_expert_act(ctx, fmt, *self.x, P, dm, g, gs, u, us, dff, self.h, g_scale=gg, u_scale=gu, **seg)
+            L.clha_fp4_expert_act(ctx, fmt, *self.x, P, dm, g, gs, u, us, dff, self.h, x_scale=xs, g_scale=gg, u_scale=gu,
+                                  **seg)
         with t.span("quantize"):
-            L.clha_fp4_quantize(ctx, self.h, P, dff, fmt, *self.hq, **seg)
+            L.clha_fp4_quantize(ctx, self.h, P, dff, fmt, *self.hq, tensor_scale=hs, **seg)
         with t.span("down"):
-            L.clha_fp4_matmul(ctx, fmt, *self.hq, P, dff, d, ds, dm, self.z, w_scale=gd, **seg)
+            L.clha_fp4_matmul(ctx, fmt, *self.hq, P, dff, d, ds, dm, self.z, x_scale=hs, w_scale=gd, **seg)
         add = None
         if self.shared:
             sd, add = self.shared, self.sy[:n]
             (g, gs, gg), (u, us, gu), (d, ds, gd) = *self.s_gate_up, self.s_down
             with t.span("shared"):
-                L.clha_fp4_quantize(ctx, X, n, dm, fmt, *self.sx)
-                L.clha_fp4_expert_act(ctx, fmt, *self.sx, n, dm, g, gs, u, us, sd, self.sh, g_scale=gg, u_scale=gu)
-                L.clha_fp4_quantize(ctx, self.sh, n, sd, fmt, *self.shq)
-                L.clha_fp4_matmul(ctx, fmt, *self.shq, n, sd, d, ds, dm, add, w_scale=gd)
+                L.clha_fp4_quantize(ctx, X, n, dm, fmt, *self.sx, tensor_scale=xs)
+                L.clha_fp4_expert_act(ctx, fmt, *self.sx, n, dm, g, gs, u, us, sd, self.sh, x_scale=xs, g_scale=gg, u_scale=gu)
+                L.clha_fp4_quantize(ctx, self.sh, n, sd, fmt, *self.shq, tensor_scale=hs)
+                L.clha_fp4_matmul(ctx, fmt, *self.shq, n, sd, d, ds, dm, add, x_scale=hs, w_scale=gd)
         with t.span("combine"):
             L.clha_combine(ctx, self.z, P, dm, ids, weights, n, k, E, self.seg, self.perm, Y, add=add)
         return Y

@@ -581,14 +581,17 @@ def quantized_weight(W, fmt):
 
 
 @pytest.mark.parametrize("fmt", FMTS)
-@pytest.mark.parametrize("n,E,k,dm,dff,ns,sdff", [(1, 8, 2, 256, 128, 0, 0), (37, 16, 2, 384, 256, 2, 128),
-                                                  (700, 8, 3, 256, 384, 1, 256)])
-def test_layer(ctx, fmt, n, E, k, dm, dff, ns, sdff):
+@pytest.mark.parametrize("n,E,k,dm,dff,ns,sdff,gx,gh", [
+    (1, 8, 2, 256, 128, 0, 0, None, None), (37, 16, 2, 384, 256, 2, 128, None, 1.7e-3),
+    (700, 8, 3, 256, 384, 1, 256, 0.013, None)])
+def test_layer(ctx, fmt, n, E, k, dm, dff, ns, sdff, gx, gh):
     """The calls together, each stage against the oracle on the stage's own inputs as the GPU left them (so that
     a 4-bit code on a border, decided by float32 sums, is not carried on)."""
     from post_quantization_expert_b200.pipeline import Fp4Layer
     w, X, lg = layer_case(n, E, k, dm, dff, ns, sdff)
-    layer = Fp4Layer(ctx, to_dev(w), k, max_tokens=n + 5, fmt=FMT[fmt], score=L.SCORE_SIGMOID, scale=1.5)
+    scales = {a: None if g is None else torch.tensor([g], device=DEV) for a, g in (("x_scale", gx), ("h_scale", gh))}
+    gx, gh = (1.0 if g is None else float(np.float32(g)) for g in (gx, gh))
+    layer = Fp4Layer(ctx, to_dev(w), k, max_tokens=n + 5, fmt=FMT[fmt], score=L.SCORE_SIGMOID, scale=1.5, **scales)
     Y = torch.full((n, dm), 5.0, device=DEV)
     assert layer.forward(X.to(DEV), lg.to(DEV), Y) is Y
     L.clha_check(ctx)
@@ -599,16 +602,16 @@ def test_layer(ctx, fmt, n, E, k, dm, dff, ns, sdff):
     end = int(seg[E])
     x64 = np.where((perm[:end] >= 0)[:, None], to64(X)[np.maximum(perm[:end], 0)], 0.0)
     W = [quantized_weight(t, fmt) for t in (w.Wg, w.Wu, w.Wd)]
-    check_act(layer.h[:end], O.fp4_values(*O.fp4_quantize(x64, fmt), fmt), W[0], W[1], seg, dm)
-    h64 = O.fp4_values(*O.fp4_quantize(to64(layer.h[:end]), fmt), fmt)
+    check_act(layer.h[:end], O.fp4_values(*O.fp4_quantize(x64, fmt, gx), fmt, gx), W[0], W[1], seg, dm)
+    h64 = O.fp4_values(*O.fp4_quantize(to64(layer.h[:end]), fmt, gh), fmt, gh)
     check_product(layer.z[:end], O.expert_products(h64, W[2], seg), O.expert_products(np.abs(h64), np.abs(W[2]), seg), dff,
                   F32)
     add = mags = None
     if ns:
         S = [quantized_weight(t.reshape(1, ns * sdff, dm), fmt) for t in (w.Sg, w.Su)]
         S.append(quantized_weight(w.Sd.permute(1, 0, 2).reshape(1, dm, ns * sdff).contiguous(), fmt))
-        check_act(layer.sh[:n], O.fp4_values(*O.fp4_quantize(to64(X), fmt), fmt), S[0], S[1], None, dm)
-        hs = O.fp4_values(*O.fp4_quantize(to64(layer.sh[:n]), fmt), fmt)
+        check_act(layer.sh[:n], O.fp4_values(*O.fp4_quantize(to64(X), fmt, gx), fmt, gx), S[0], S[1], None, dm)
+        hs = O.fp4_values(*O.fp4_quantize(to64(layer.sh[:n]), fmt, gh), fmt, gh)
         add, mags = hs @ S[2][0].T, np.abs(hs) @ np.abs(S[2][0]).T
     z64 = to64(layer.z)
     got_w = to64(layer.weights[:n])
@@ -621,7 +624,7 @@ def test_layer(ctx, fmt, n, E, k, dm, dff, ns, sdff):
         layer.forward(X.to(DEV).repeat(2 * (n + 6) // n + 1, 1), lg.to(DEV), Y)
     one = torch.full((1, dm), 5.0, device=DEV)      # fewer tokens after more: the buffers hold the earlier call's rows
     layer.forward(X[:1].to(DEV).contiguous(), lg[:1].to(DEV).contiguous(), one)
-    fresh = Fp4Layer(ctx, to_dev(w), k, max_tokens=1, fmt=FMT[fmt], score=L.SCORE_SIGMOID, scale=1.5)
+    fresh = Fp4Layer(ctx, to_dev(w), k, max_tokens=1, fmt=FMT[fmt], score=L.SCORE_SIGMOID, scale=1.5, **scales)
     assert torch.equal(one, fresh.forward(X[:1].to(DEV).contiguous(), lg[:1].to(DEV).contiguous(), torch.empty_like(one)))
     empty = torch.empty((0, dm), device=DEV)
     layer.forward(empty, torch.empty((0, E), device=DEV), empty)
