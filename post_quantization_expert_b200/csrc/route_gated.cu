@@ -78,13 +78,13 @@ __device__ __forceinline__ void warp_best(F& v, int& i) {
 }
 
 // Bound on the difference of two float32 choices whose exact order it leaves open. A sigmoid, 1 / (1 + e), is off by
-// less than 2^-24 through e (2^-22 of it, times s (1 - s) <= 1/4) and 2^-23 of itself through the sum and the
-// division: 2^-22. A softmax is off by less than 2^-18 of the largest score: 2^-22 and the rounded argument's
-// 0.37 2^-24 through the exponential, as much through the sum, whose up to 37 roundings add 37 2^-24, and 2^-22
-// through the division and the product. A biased choice adds 2^-24 of its size. Twice that for the two.
-// (Sums of two are off by twice as much and a rounding of their own: three times the bound.)
+// less than 2^-24 through e (two steps, 2^-22 of it, times s (1 - s) <= 1/4), 2^-24 through the sum and 2^-22 through
+// the fast division (two steps): 1.5 2^-22. A softmax is off by less than 2^-18 of the largest score: 2^-22 and the
+// rounded argument's 0.37 2^-24 through the exponential, as much through the sum, whose up to 37 roundings add
+// 37 2^-24, and 2^-23 through the division and the product. A biased choice adds 2^-24 of its size. Twice that, or
+// more, for the two. (Sums of two are off by twice as much and a rounding of their own: three times the bound.)
 __device__ __forceinline__ float choice_slack(bool sigmoid, float top_score, float largest_choice) {
-    return (sigmoid ? 0x1p-21f : 0x1p-17f * top_score) + 0x1p-23f * largest_choice;
+    return (sigmoid ? 0x1p-20f : 0x1p-17f * top_score) + 0x1p-23f * largest_choice;
 }
 
 // One token's selection by a warp, in float32. Lane j < k (and j + 32, ...) writes the j-th expert and its
