@@ -82,7 +82,8 @@ __device__ __forceinline__ void warp_best(F& v, int& i) {
 // the fast division (two steps): 1.5 2^-22. A softmax is off by less than 2^-18 of the largest score: 2^-22 and the
 // rounded argument's 0.37 2^-24 through the exponential, as much through the sum, whose up to 37 roundings add
 // 37 2^-24, and 2^-23 through the division and the product. A biased choice adds 2^-24 of its size. Twice that, or
-// more, for the two. (Sums of two are off by twice as much and a rounding of their own: three times the bound.)
+// more, for the two. (Sums of two are off by twice as much and a rounding of their own, of up to twice the size:
+// four times the bound.)
 __device__ __forceinline__ float choice_slack(bool sigmoid, float top_score, float largest_choice) {
     return (sigmoid ? 0x1p-20f : 0x1p-17f * top_score) + 0x1p-23f * largest_choice;
 }
@@ -177,7 +178,7 @@ __device__ __forceinline__ bool select_token(const GateArgs& p, const float (&l)
                 if ((open >> i & 1) && (bi == 0x7fffffff || rank[i] > bv)) { bv = rank[i]; bi = lane + 32 * i; }
             warp_best(bv, bi);
             if (r == p.top_groups) {
-                if (!by_logit && last - bv <= 3 * slack) return false;
+                if (!by_logit && last - bv <= 4 * slack) return false;
                 break;
             }
             last = bv;
@@ -550,7 +551,7 @@ __global__ void __launch_bounds__(kWarps * 32, VPL == 8 ? 4 : 2) route_lanes_ker
             if (!by_logit && p.top_groups < p.n_groups) {    // the last kept and the first dropped rank
                 const float above = -lanes_max<LPT>(kept ? -rank : -INFINITY);
                 const float below = lanes_max<LPT>(in && !kept ? rank : -INFINITY);
-                open = above - below <= 3 * slack;
+                open = above - below <= 4 * slack;
             }
             const unsigned stay = __ballot_sync(kAll, kept) >> first;   // by lanes
             if (p.group_lanes) {
