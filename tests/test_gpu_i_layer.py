@@ -103,6 +103,19 @@ def test_quantize_borders(ctx, fmt, g):
 
 
 @pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("dtype", [BF16, F32])
+def test_quantize_every_exponent(ctx, fmt, dtype):
+    """A row for each exponent of the type, subnormal ones among them, with values down to far below the largest."""
+    r = np.random.default_rng(3)
+    e = np.arange(-149 if dtype == F32 else -133, 128)
+    x = np.ldexp(1 + r.random((len(e), 256)), e[:, None] - r.integers(0, 9, (len(e), 256))) * r.choice([-1, 1], (len(e), 256))
+    x = torch.from_numpy(np.clip(x, -3.3e38, 3.3e38)).to(dtype)
+    codes, scales = quantize(ctx, x.to(DEV), fmt)
+    check_quantized(codes, scales, to64(x), fmt)
+    L.clha_check(ctx)
+
+
+@pytest.mark.parametrize("fmt", FMTS)
 def test_quantize_routed_rows(ctx, fmt):
     """Rows through a permutation, segments with padding and empty experts, rows behind the last segment."""
     n, E, k, d = 300, 10, 3, 384
