@@ -672,6 +672,15 @@ cudaError_t launch_pair(cudaStream_t s, int num_sms, const Fp4Product& a, int* e
     return cudaGetLastError();
 }
 
+// CTAs of a cluster that share a tile's K in the kernel for few rows, `places` being the CTAs that run at one time:
+// as many as find a place. Clusters of 8 leave an eighth of the places or more unused (a cluster stays within a
+// GPC): 16 of them, of one CTA an SM, took 25 us where clusters of 4 take 17 (256 x 16384 -> 1024).
+int few_split(int64_t tiles, int64_t places, int nk) {
+    int split = 1;
+    while (split < 8 && tiles * split * 2 <= (split == 4 ? places * 3 / 4 : places) && nk >= 4 * split) split *= 2;
+    return split;
+}
+
 template <int BLOCK, int NB, int XR, typename OUT>
 cudaError_t launch_few(cudaStream_t s, int num_sms, const Fp4Product& a, int* err) {
     using C = Cfg<BLOCK, NB, XR>;
@@ -684,10 +693,9 @@ cudaError_t launch_few(cudaStream_t s, int num_sms, const Fp4Product& a, int* er
     MatmulArgs p{a.rows, a.K, a.N, a.seg, a.E, a.xg, a.wg, a.ug, a.Y, a.N / 128, 1, err};
     const int64_t bound = (a.rows + XR - 1) / XR * p.n_tiles;            // tiles, at most
     const int64_t expect = expected_row_tiles(a, XR) * p.n_tiles;
-    const int nk = (a.K + 255) / 256;
-    const int slots = num_sms * C::CTAS;
-    while (p.split < 8 && expect * p.split * 2 <= slots && nk >= 4 * p.split) p.split *= 2;
-    const int64_t grid = p.split > 1 ? bound * p.split : (bound < slots ? bound : slots);
+    const int places = num_sms * C::CTAS;
+    p.split = few_split(expect, places, (a.K + 255) / 256);
+    const int64_t grid = p.split > 1 ? bound * p.split : (bound < places ? bound : places);
     e = clha_launch_overlapped(kernel, (unsigned)grid, kThreads, C::SMEM, s, (unsigned)p.split, t.X, t.Xs, t.W, t.Ws, t.U,
                                t.Us, p);
     if (e != cudaSuccess) return e;
@@ -698,13 +706,24 @@ cudaError_t launch_few(cudaStream_t s, int num_sms, const Fp4Product& a, int* er
 template <int BLOCK, int NB, typename OUT>
 cudaError_t launch_product(cudaStream_t s, int num_sms, const Fp4Product& a, int* err) {
     constexpr bool ACT = NB == 2;
-    const int tile_n = ACT ? 128 : 256;
-    // pairs where there is a tile for each and its 256 rows are not mostly empty
-    const bool full = a.seg ? slots_of(a) >= 128 * (int64_t)a.E : a.rows > 128;
-    if (full && expected_row_tiles(a, 256) * ((a.N + tile_n - 1) / tile_n) >= num_sms / 2)
-        return launch_pair<BLOCK, ACT, OUT>(s, num_sms, a, err);
+    // Which kernel: the one with the fewer rounds of stages, in units of a pair's stage (0.37 us). A round costs five
+    // more for its start and end. A stage of the kernel for few rows costs 1.2 with a few rows a tile, and more with
+    // more of them: 2.05 with 128, or 3.5 with 64 or more for gate and up. Measured on both sides, few against pairs:
+    // 28672 -> 8192 with 1 row 25 : 58 us, 64 rows 33 : 42, 128 rows 43 : 43, 200 rows 74 : 45; 16384 -> 1024 with 512
+    // rows 18 : 25, 1024 rows 28 : 26; gate/up 2048 -> 1408 of 64 experts, top 6, with 64 tokens 28 : 37, 256 tokens
+    // 40 : 47, 512 tokens 52 : 50, 4096 tokens 161 : 105.
+    const bool short_x = !a.seg && a.rows <= 32;
+    const int nk = (a.K + 255) / 256, tile_n = ACT ? 128 : 256, pairs = num_sms / 2;
+    const int64_t places = short_x && !ACT ? 2 * num_sms : num_sms, few_rows = expected_row_tiles(a, short_x ? 32 : 128);
+    const int64_t few_tiles = few_rows * (a.N / 128), pair_tiles = expected_row_tiles(a, 256) * ((a.N + tile_n - 1) / tile_n);
+    const int split = few_split(few_tiles, places, nk);
+    const double rows = (double)(a.seg ? slots_of(a) : a.rows) / (few_rows > 0 ? few_rows : 1);
+    const double stage = ACT ? 1.2 + 2.3 * (rows < 64 ? rows / 64 : 1) : 1.2 + 0.85 * (rows / 128);
+    const double few = (few_tiles * split + places - 1) / places * ((nk + split - 1) / split * stage + 5);
+    const double pair = (pair_tiles + pairs - 1) / pairs * (nk + 5.0);
+    if (pair <= few) return launch_pair<BLOCK, ACT, OUT>(s, num_sms, a, err);
     // up to 32 dense rows: room for W's copies instead of 128 rows of X
-    if (!a.seg && a.rows <= 32) return launch_few<BLOCK, NB, 32, OUT>(s, num_sms, a, err);
+    if (short_x) return launch_few<BLOCK, NB, 32, OUT>(s, num_sms, a, err);
     return launch_few<BLOCK, NB, 128, OUT>(s, num_sms, a, err);
 }
 

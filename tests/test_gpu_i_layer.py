@@ -227,7 +227,9 @@ def check_product(got, want, mags, K, out):
 @pytest.mark.parametrize("n,K,N", [(1, 128, 128), (1, 2048, 256), (7, 384, 384), (128, 256, 128), (129, 640, 256),
                                    (300, 1152, 640), (64, 8192, 128),
                                    # many tiles: pairs of SMs, the last row tile and the last column block halves
-                                   (2600, 640, 2176), (4999, 1152, 1024)])
+                                   (2600, 640, 2176), (4999, 1152, 1024),
+                                   # a long K over few tiles: clusters of 8 and 4 share it, three row tiles
+                                   (300, 8192, 128), (70, 4224, 384), (32, 3968, 1024), (33, 2176, 128)])
 def test_matmul(ctx, fmt, out, n, K, N):
     x = torch.randn((n, K), generator=gen(n + K)).to(BF16)
     w = (0.02 * torch.randn((N, K), generator=gen(N))).to(BF16)
@@ -249,6 +251,9 @@ def stacked(w, E):
                                        (1500, 4, 2, 256, 640),
                                        # many tiles: pairs of SMs, segments with an odd number of 128-row tiles
                                        (3001, 10, 3, 384, 640), (2000, 64, 6, 256, 384),
+                                       # few rows an expert: with K shared by clusters, and without
+                                       (5, 16, 2, 2048, 128), (40, 64, 6, 2048, 128), (1, 8, 8, 1920, 384),
+                                       (100, 16, 2, 1024, 1280),
                                        # the most experts
                                        (1100, 1024, 130, 128, 128)])
 def test_expert_products(ctx, fmt, scaled, n, E, k, K, N):
@@ -298,7 +303,8 @@ def check_act(h, x64, w64, u64, seg, K):
 
 
 @pytest.mark.parametrize("fmt", FMTS)
-@pytest.mark.parametrize("n,K,N", [(1, 2048, 128), (3, 4096, 256), (130, 128, 384), (257, 640, 128), (2570, 384, 1024)])
+@pytest.mark.parametrize("n,K,N", [(1, 2048, 128), (3, 4096, 256), (130, 128, 384), (257, 640, 128), (2570, 384, 1024),
+                                   (130, 4224, 128)])
 def test_dense_act(ctx, fmt, n, K, N):
     x = torch.randn((n, K), generator=gen(n)).to(BF16)
     w, u = ((0.05 * torch.randn((N, K), generator=gen(i))).to(BF16) for i in (21, 22))
