@@ -70,10 +70,9 @@ __device__ __forceinline__ bool mbar_wait_bounded(uint32_t bar, uint32_t parity,
 }
 
 // ------------------------------------------------------------------------------ warp-uniform issue
-// A role whose whole warp runs its loop, with one elected lane issuing, keeps addresses and descriptors in uniform
-// registers; under `if (lane == 0)` each operand of each tcgen05 instruction is moved there one by one first (a
-// block-scaled product and its share of waits and commits then takes about 180 cycles to issue, more than it
-// takes to run).
+// A role whose whole warp runs its loop, with one elected lane issuing: tcgen05 takes its addresses and descriptors
+// from uniform registers, and a loop that the whole warp runs can keep them there. Under `if (lane == 0)` a
+// block-scaled product with its share of waits and commits took about 180 cycles to issue, whatever its size.
 __device__ __forceinline__ bool elect_one() {
     uint32_t p;
     asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(p));
