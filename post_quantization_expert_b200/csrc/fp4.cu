@@ -285,14 +285,15 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 4 : 2) fp4_quantize
     constexpr int LPB = BLOCK / 16;                          // lanes a block
     const int atoms = p.d / BLOCK / 4;                       // 512-byte scale tiles across a row tile
     extern __shared__ int before[];
-    if (p.bands > 1) band_table(p, before);
+    const bool in_bands = p.bands > 1 && p.seg[p.E] <= p.rows;   // (segments that `rows` cuts off: tiles as they lie)
+    if (in_bands) band_table(p, before);
     // a unit: the 128 rows of a tile, rows r, r + 32, r + 64, r + 96 to eight lanes, by p.run columns
     const int runs = (p.d + p.run - 1) / p.run;
     for (int64_t u = blockIdx.x;; u += gridDim.x) {
         int64_t tile = u / runs;
         const int c0 = (int)(u - tile * runs) * p.run, c1 = min(p.d, c0 + p.run);
         if (tile * 128 >= live) break;
-        if (p.bands > 1) tile = banded(p, before, tile);
+        if (in_bands) tile = banded(p, before, tile);
         const int64_t r0 = tile * 128 + r;
         const T* src[4];                                       // null: a row of zeros
         uint8_t* dst[4];                                       // null: behind the last row

@@ -153,6 +153,25 @@ def test_quantize_routed_rows_of_a_large_x(ctx, fmt, n, E, k, d, dtype):
 
 
 @pytest.mark.parametrize("fmt", FMTS)
+def test_quantize_only_the_first_routed_rows(ctx, fmt):
+    """Fewer rows than the segments hold, of an X that is large enough for another order of the tiles."""
+    n, E, k, d = 9000, 24, 3, 4096
+    ids, seg, perm = route(n, E, k, 5)
+    rows = 128 * 100 + 37
+    assert n < rows < int(seg[E])
+    x = torch.randn((n, d), generator=torch.Generator(device=DEV).manual_seed(1), device=DEV).to(BF16)
+    codes, scales = buffers(fmt, rows + 200, d)
+    L.clha_fp4_quantize(ctx, x, n, d, FMT[fmt], codes, scales, perm=torch.from_numpy(perm).to(DEV), rows=rows,
+                        seg=torch.from_numpy(seg).to(DEV), E=E)
+    p = torch.from_numpy(perm[:rows]).to(DEV)
+    xp = torch.where((p >= 0)[:, None], x[p.clamp_min(0).long()], torch.zeros((), dtype=BF16, device=DEV))
+    want_c, want_s = quantize(ctx, xp, fmt)
+    assert torch.equal(codes[:rows], want_c) and torch.equal(scales[:want_s.numel()], want_s)
+    assert (codes[rows:] == 0xA5).all() and (scales[want_s.numel():] == 0xA5).all()
+    L.clha_check(ctx)
+
+
+@pytest.mark.parametrize("fmt", FMTS)
 def test_quantize_batch_of_scales_and_dequantize(ctx, fmt):
     """Three matrices with a scale each: clha_fp4_tensor_scale, the codes under them, and their values."""
     B, rows, d = 3, 130, 256
