@@ -371,7 +371,7 @@ typedef struct {
     float scale;
 } clha_route_params;
 
-/* Top-k routing with gate weights. For each of n tokens, of its router logits l [n, E] (f32 or bf16): the
+/* Top-k routing with gate weights. For each of n tokens (n < 2^31), of its router logits l [n, E] (f32 or bf16): the
  * scores s = softmax(l) or sigmoid(l), the choices c = s + bias (bias: float32 [E] or NULL), and the k
  * experts of the largest choices, in descending order, ties to the lower expert (and group). ids [n, k]
  * int32 are the experts, weights [n, k] float32 their scores (without the bias; 1/k each if renormalised

@@ -687,7 +687,7 @@ extern "C" clha_status clha_route_gated(clha_ctx* ctx, const void* logits, clha_
     CHECK_CTX(ctx);
     REQUIRE(rp, CLHA_ERR_INVALID_ARG, "clha_route_gated: null params");
     REQUIRE(dtype_size(dtype), CLHA_ERR_INVALID_ARG, "clha_route_gated: unknown dtype");
-    REQUIRE(n >= 0, CLHA_ERR_INVALID_ARG, "clha_route_gated: n < 0");
+    REQUIRE(n >= 0 && n < (int64_t)1 << 31, CLHA_ERR_INVALID_ARG, "clha_route_gated: n must be in 0..2^31 - 1");
     REQUIRE(rp->E >= 1 && rp->E <= 1024, CLHA_ERR_INVALID_ARG, "clha_route_gated: E must be in 1..1024");
     REQUIRE(rp->score == CLHA_SCORE_SOFTMAX || rp->score == CLHA_SCORE_SIGMOID, CLHA_ERR_INVALID_ARG,
             "clha_route_gated: unknown score");

@@ -81,12 +81,19 @@ __device__ __forceinline__ void warp_best(F& v, int& i) {
 // less than 2^-24 through e (two steps, 2^-22 of it, times s (1 - s) <= 1/4), 2^-24 through the sum and 2^-22 through
 // the fast division (two steps): 1.5 2^-22. A softmax is off by less than 2^-18 of the largest score: 2^-22 and the
 // rounded argument's 0.37 2^-24 through the exponential, as much through the sum, whose up to 37 roundings add
-// 37 2^-24, and 2^-23 through the division and the product. A biased choice adds 2^-24 of its size. Twice that, or
-// more, for the two. (Sums of two are off by twice as much and a rounding of their own, of up to twice the size:
-// four times the bound.)
-__device__ __forceinline__ float choice_slack(bool sigmoid, float top_score, float largest_choice) {
-    return (sigmoid ? 0x1p-20f : 0x1p-17f * top_score) + 0x1p-23f * largest_choice;
+// 37 2^-24, and 2^-23 through the division and the product. Twice that, or more, for the two.
+__device__ __forceinline__ float choice_slack(bool sigmoid, float top_score) {
+    return sigmoid ? 0x1p-20f : 0x1p-17f * top_score;
 }
+// A biased choice adds 2^-24 of its own size. That of the lower one counts: the upper exceeds it by their distance at
+// most. (So a bias of float32's lowest value, which shuts an expert out, leaves the others' order alone. The first round
+// compares with +inf, the round behind the last expert with -inf: not near.)
+__device__ __forceinline__ bool too_near(float above, float below, float slack) {
+    return above - below < fmaf(0x1p-22f, fabsf(below), slack);
+}
+// Half-width of the interval of a group's rank, a choice or the sum of two whose larger size is `size`: a sum is off by
+// twice a choice's error, half the slack each, and by a rounding of its own of 2^-24 of up to twice the size.
+__device__ __forceinline__ float rank_error(float slack, float size) { return fmaf(0x1p-21f, size, 2 * slack); }
 
 // One token's selection by a warp, in float32. Lane j < k (and j + 32, ...) writes the j-th expert and its
 // weight. Returns false, with nothing written, where a decision was nearer than the error bound.
@@ -116,7 +123,6 @@ __device__ __forceinline__ bool select_token(const GateArgs& p, const float (&l)
         for (int i = 0; i < VPL; ++i) s[i] = lane + 32 * i < p.E ? 1 / (1 + expf(-l[i])) : 0;
     }
     unsigned live = 0;   // bit i: expert lane + 32 i may be chosen
-    float big = 0;
 #pragma unroll
     for (int i = 0; i < VPL; ++i) {
         const int e = lane + 32 * i;
@@ -129,21 +135,19 @@ __device__ __forceinline__ bool select_token(const GateArgs& p, const float (&l)
                     c[i] += b;
                 else                                          // recorded; taken as 0
                     clha_record_error(p.err, CLHA_ERR_NONFINITE, (int)(t & 0x7fffffff), e, KID_GATE);
-                big = fabsf(c[i]) > big ? fabsf(c[i]) : big;
             }
         }
     }
-    float slack = 0;
-    if (!by_logit) slack = choice_slack(p.sigmoid != 0, top_score, warp_max(big));
+    const float slack = choice_slack(p.sigmoid != 0, top_score);
 
     if (p.n_groups > 1) {
         // rank every group (all lanes hold it), then keep the first top_groups
         const int size = p.E / p.n_groups;
-        float rank[VPL];     // lane holds groups lane, lane + 32, ...
+        float rank[VPL], off[VPL];   // lane holds groups lane, lane + 32, ...; half-widths of the ranks' intervals
         unsigned open = 0;
 #pragma unroll
         for (int i = 0; i < VPL; ++i) {
-            rank[i] = 0;
+            rank[i] = off[i] = 0;
             if (lane + 32 * i < p.n_groups) open |= 1u << i;
         }
         for (int g = 0; g < p.n_groups; ++g) {
@@ -163,26 +167,30 @@ __device__ __forceinline__ bool select_token(const GateArgs& p, const float (&l)
                 b = b < ob ? ob : b;
                 b = b < lo ? lo : b;
             }
-            const float r = p.top2 && size > 1 ? a + b : a;
+            const bool two = p.top2 && size > 1;
+            const float r = two ? a + b : a, o = rank_error(slack, two ? fmaxf(fabsf(a), fabsf(b)) : fabsf(a));
 #pragma unroll
             for (int i = 0; i < VPL; ++i)
-                if (g == lane + 32 * i) rank[i] = r;
+                if (g == lane + 32 * i) { rank[i] = r; off[i] = o; }
         }
         unsigned kept = 0;
-        float last = 0;
-        for (int r = 0; r <= p.top_groups && r < p.n_groups; ++r) {
+        float above = INFINITY, below = -INFINITY;            // the kept ranks' lowest, the others' highest bound
+        for (int r = 0; r < p.top_groups; ++r) {
             float bv = 0;
             int bi = 0x7fffffff;
 #pragma unroll
             for (int i = 0; i < VPL; ++i)
                 if ((open >> i & 1) && (bi == 0x7fffffff || rank[i] > bv)) { bv = rank[i]; bi = lane + 32 * i; }
             warp_best(bv, bi);
-            if (r == p.top_groups) {
-                if (!by_logit && last - bv <= 4 * slack) return false;
-                break;
-            }
-            last = bv;
             if ((bi & 31) == lane) { open &= ~(1u << (bi >> 5)); kept |= 1u << (bi >> 5); }
+        }
+        if (!by_logit && p.top_groups < p.n_groups) {
+#pragma unroll
+            for (int i = 0; i < VPL; ++i) {
+                if (kept >> i & 1) above = fminf(above, rank[i] - off[i]);
+                if (open >> i & 1) below = fmaxf(below, rank[i] + off[i]);
+            }
+            if (!(-warp_max(-above) > warp_max(below))) return false;   // (sums that overflow: -inf on both sides)
         }
 #pragma unroll
         for (int i = 0; i < VPL; ++i) {
@@ -204,7 +212,7 @@ __device__ __forceinline__ bool select_token(const GateArgs& p, const float (&l)
             if ((live >> i & 1) && (bi == 0x7fffffff || c[i] > bv)) { bv = c[i]; bi = lane + 32 * i; }
         warp_best(bv, bi);
         if (bi == 0x7fffffff) break;
-        if (!by_logit && r > 0 && last - bv <= slack) open_order = true;
+        if (!by_logit && r > 0 && too_near(last, bv, slack)) open_order = true;
         if (r == p.k || open_order) break;
         last = bv;
         float sv = 0;
@@ -492,22 +500,21 @@ __global__ void __launch_bounds__(kWarps * 32, VPL == 8 ? 4 : 2) route_lanes_ker
         const auto score = [&](float l) {
             return p.sigmoid ? __fdividef(1.f, 1.f + expf(-l)) : expf(l - m) * top_score;
         };
-        float slack = 0.f;
+        const float slack = choice_slack(p.sigmoid != 0, top_score);
         if (!by_logit) {
-            float big = 0.f;
 #pragma unroll
             for (int i = 0; i < VPL; ++i)
-                if (e0 + i < p.E) {
-                    c[i] = score(c[i]) + (p.bias ? bias[i] : 0.f);
-                    big = fmaxf(big, fabsf(c[i]));
-                }
-            slack = choice_slack(p.sigmoid != 0, top_score, lanes_max<LPT>(big));
+                if (e0 + i < p.E) c[i] = score(c[i]) + (p.bias ? bias[i] : 0.f);
         }
         bool open = false;                                   // a decision inside the error bound
         if (p.n_groups > 1) {
             const int size = p.E / p.n_groups;
             const int q = p.group_lanes ? p.group_lanes : 1; // lanes a group, a power of two; or lane h has group h's rank
-            float rank = -INFINITY;
+            float rank = -INFINITY, off = 0.f;               // and the half-width of its interval
+            const auto set_rank = [&](float a, float b, bool two) {
+                rank = two ? a + b : a;
+                off = rank_error(slack, two ? fmaxf(fabsf(a), fabsf(b)) : fabsf(a));
+            };
             if (p.group_lanes) {
                 float a = -INFINITY, b = -INFINITY;          // the two largest choices of the group
 #pragma unroll
@@ -520,7 +527,7 @@ __global__ void __launch_bounds__(kWarps * 32, VPL == 8 ? 4 : 2) route_lanes_ker
                     b = fmaxf(fmaxf(b, ob), fminf(a, oa));
                     a = fmaxf(a, oa);
                 }
-                if (e0 < p.E) rank = p.top2 ? a + b : a;
+                if (e0 < p.E) set_rank(a, b, p.top2);
             } else {
                 for (int h = 0; h < p.n_groups; ++h) {
                     const unsigned from = h * size - e0;     // the group's first expert among this lane's
@@ -537,7 +544,7 @@ __global__ void __launch_bounds__(kWarps * 32, VPL == 8 ? 4 : 2) route_lanes_ker
                         b = fmaxf(fmaxf(b, ob), fminf(a, oa));
                         a = fmaxf(a, oa);
                     }
-                    if (sub == h) rank = p.top2 && size > 1 ? a + b : a;
+                    if (sub == h) set_rank(a, b, p.top2 && size > 1);
                 }
             }
             const int g = sub / q;
@@ -548,10 +555,10 @@ __global__ void __launch_bounds__(kWarps * 32, VPL == 8 ? 4 : 2) route_lanes_ker
                 ahead += r > rank || (r == rank && h < g);
             }
             const bool kept = in && ahead < p.top_groups;
-            if (!by_logit && p.top_groups < p.n_groups) {    // the last kept and the first dropped rank
-                const float above = -lanes_max<LPT>(kept ? -rank : -INFINITY);
-                const float below = lanes_max<LPT>(in && !kept ? rank : -INFINITY);
-                open = above - below <= 4 * slack;
+            if (!by_logit && p.top_groups < p.n_groups) {    // the kept ranks' lowest, the others' highest bound
+                const float above = -lanes_max<LPT>(kept ? off - rank : -INFINITY);
+                const float below = lanes_max<LPT>(in && !kept ? rank + off : -INFINITY);
+                open = !(above > below);                     // (sums that overflow: -inf on both sides)
             }
             const unsigned stay = __ballot_sync(kAll, kept) >> first;   // by lanes
             if (p.group_lanes) {
@@ -576,7 +583,7 @@ __global__ void __launch_bounds__(kWarps * 32, VPL == 8 ? 4 : 2) route_lanes_ker
 #pragma unroll
             for (int i = 1; i < VPL; ++i) mx = fmaxf(mx, c[i]);
             const float best = lanes_max<LPT>(mx);
-            if (last - best <= slack && !by_logit) open = true;
+            if (too_near(last, best, slack) && !by_logit) open = true;
             last = best;
             const int owner = __ffs(__ballot_sync(kAll, mx == best) & mine) - 1;
             int idx = 0;
@@ -594,8 +601,8 @@ __global__ void __launch_bounds__(kWarps * 32, VPL == 8 ? 4 : 2) route_lanes_ker
         float f = p.scale;
         if (p.renorm) {
             const float sum = lanes_sum<LPT>(s0 + s1);
-            if (!(sum > 1e-30f)) open = true;                // float32 scores that underflow
             f = p.scale / sum;
+            if (!(sum > 1e-30f && fabsf(f) < INFINITY)) open = true;   // float32 scores that underflow
         }
         if (real && !open) {
             if (has0) {

@@ -6,6 +6,8 @@ products' sums are float32 on the tensor cores: 64 columns are added to the accu
 most one truncation of 2^-23 of the larger operand each, so K columns give at most (K / 64 + 64) 2^-23 of
 the sum of the terms' magnitudes |x| |w|^T.
 """
+import ctypes
+
 import numpy as np
 import pytest
 import torch
@@ -434,6 +436,31 @@ def test_route_extreme_logits(ctx):
     check_route(ctx, torch.full((2, E), -100.0), 4, 0.1 * torch.randn(E, generator=gen(1)), score="sigmoid")
 
 
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("E,groups,top,rank", [(64, 1, 1, "max"), (64, 4, 2, "max"), (64, 4, 2, "top2"), (30, 5, 2, "top2"),
+                                               (600, 6, 3, "top2"), (600, 1, 1, "max")])
+def test_route_biases_of_the_lowest_value(ctx, score, E, groups, top, rank):
+    """Experts shut out by a bias of float32's lowest value; fewer open ones than k; group sums past float32's range,
+    whose order only the float64 values show."""
+    k, low = 6, torch.finfo(F32).min
+    l = torch.randn((90, E), generator=gen(E + groups))
+    kw = dict(score=score, n_groups=groups, top_groups=top, group_rank=rank)
+    bias = 0.2 * torch.randn(E, generator=gen(E))
+    some = torch.rand(E, generator=gen(E + 1)) < 0.4
+    check_route(ctx, l, k, torch.where(some, low, bias), **kw)
+    check_route(ctx, l, k, torch.where(torch.arange(E) < E - 3, low, bias), **kw)
+    by_group = torch.linspace(1.0, 0.6, groups).mul(low).repeat_interleave(E // groups)      # the last groups first
+    check_route(ctx, l, k, by_group, **kw)
+    check_route(ctx, l, k, -by_group, **kw)
+    check_route(ctx, l, k, torch.full((E,), low), **kw)
+
+
+def test_route_scale_over_a_small_sum(ctx):
+    """A scale over a sum that leaves float32 where the weights do not."""
+    l = torch.randn((20, 64), generator=gen(5)) - 60
+    check_route(ctx, l, 4, None, score="sigmoid", scale=1e20)
+
+
 def test_route_reports_non_finite(ctx):
     E, k = 40, 4
     for where, v in (("l", float("nan")), ("l", float("inf")), ("l", -float("inf")), ("b", float("nan"))):
@@ -561,6 +588,9 @@ def test_refusals(ctx):
         with pytest.raises(L.ClhaError) as ei:
             call()
         assert ei.value.status == status, (i, ei.value)
+    params = L._route_params(E, k, L.SCORE_SOFTMAX, 1, 1, L.GROUP_MAX, True, 1.0)     # more tokens than a count holds
+    assert L.load().clha_route_gated(ctx.handle, lg.data_ptr(), L.F32, 2 ** 31, ctypes.byref(params), None, ids.data_ptr(),
+                                     w.data_ptr(), counts.data_ptr()) == A
     with pytest.raises(ValueError):        # a non-contiguous tensor
         L.clha_fp4_quantize(ctx, torch.randn((d, n), device=DEV).T, n, d, f, q, s)
     with pytest.raises(TypeError):         # half-precision inputs are not taken
