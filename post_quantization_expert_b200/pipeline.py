@@ -653,7 +653,14 @@ class Fp4Layer:
         self.gate = dict(score=score, bias=bias, n_groups=n_groups, top_groups=top_groups, group_rank=group_rank,
                          renormalise=renormalise, scale=scale)
         dev = self.dev = torch.device("cuda", ctx.device)
-        E, dm, dff = self.E, self.d_model, self.d_ff
+        # on the context's stream, behind what the caller has queued for the weights: buffers and the copies of weights
+        # that are quantized and dropped then belong to the stream that uses them
+        ctx.stream.wait_stream(torch.cuda.current_stream(dev))
+        with torch.cuda.stream(ctx.stream):
+            self._build(w, max_tokens, k)
+
+    def _build(self, w: MoEWeights, max_tokens: int, k: int):
+        dev, E, dm, dff = self.dev, self.E, self.d_model, self.d_ff
         self.gate_up = [self._weight(m, E, dff, dm) for m in (w.Wg, w.Wu)]
         self.down = self._weight(w.Wd, E, dm, dff)
         self.P = L.clha_packed_rows(max_tokens, k, E)

@@ -747,6 +747,34 @@ def test_layer_captured_and_on_other_streams(ctx):
     c2.close()
 
 
+def test_layer_built_on_another_stream(ctx):
+    """Weights that the current stream has yet to write, quantized on the context's own stream."""
+    from post_quantization_expert_b200.pipeline import Fp4Layer
+    n, E, k, dm, dff = 40, 8, 2, 256, 256
+    w, X, lg = layer_case(n, E, k, dm, dff, 2, 128)
+    wd, x, l = to_dev(w), X.to(DEV), lg.to(DEV)
+    want = Fp4Layer(ctx, wd, k, n).forward(x, l, torch.empty((n, dm), device=DEV))
+    late, busy = to_dev(w), torch.zeros((8192, 8192), dtype=BF16, device=DEV)
+    fields = [t for t in vars(late).values() if torch.is_tensor(t)]
+    kept = [t.clone() for t in fields]
+    for t in fields:
+        t.zero_()
+    torch.cuda.synchronize()
+    own = L.Context(0, torch.cuda.Stream())
+    for _ in range(20):                    # a few milliseconds
+        busy = busy @ busy
+    for t, v in zip(fields, kept):
+        t.copy_(v)
+    layer = Fp4Layer(own, late, k, n)
+    dropped = [torch.full((k_, 1 << 16), -1.0, dtype=BF16, device=DEV) for k_ in (1, 2, 3, 4)]   # reuses what was freed
+    with torch.cuda.stream(own.stream):
+        got = layer.forward(x, l, torch.empty((n, dm), device=DEV))
+    torch.cuda.synchronize()
+    assert torch.equal(got, want) and len(dropped) == 4
+    L.clha_check(own)
+    own.close()
+
+
 def test_offsets_past_32_bits(ctx):
     """Codes, scales, values and outputs whose element offsets pass 2^31: the last rows against a small call."""
     rows, d, f = 131329, 16384, L.FP4_E8M0_32          # 2.15e9 elements
