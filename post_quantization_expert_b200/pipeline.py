@@ -654,10 +654,16 @@ class Fp4Layer:
                          renormalise=renormalise, scale=scale)
         dev = self.dev = torch.device("cuda", ctx.device)
         # on the context's stream, behind what the caller has queued for the weights: buffers and the copies of weights
-        # that are quantized and dropped then belong to the stream that uses them
-        ctx.stream.wait_stream(torch.cuda.current_stream(dev))
+        # that are quantized and dropped then belong to the stream that uses them. What the caller queues next, on
+        # weights overwritten or memory handed out again, comes behind their quantization
+        current = torch.cuda.current_stream(dev)
+        ctx.stream.wait_stream(current)
         with torch.cuda.stream(ctx.stream):
             self._build(w, max_tokens, k)
+        current.wait_stream(ctx.stream)
+        for t in (w.Wgu, w.Wd, w.Sgu, w.Sd, bias, x_scale, h_scale):
+            if t is not None:
+                t.record_stream(ctx.stream)      # (allocated on any stream, dropped at any time)
 
     def _build(self, w: MoEWeights, max_tokens: int, k: int):
         dev, E, dm, dff = self.dev, self.E, self.d_model, self.d_ff

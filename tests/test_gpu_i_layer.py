@@ -804,3 +804,35 @@ def test_offsets_past_32_bits(ctx):
     L.clha_check(ctx)
     del codes, scales, y, small, xq
     torch.cuda.empty_cache()
+
+
+@pytest.mark.parametrize("how", ["overwritten", "dropped"])
+def test_layer_weights_are_the_callers_again(ctx, how):
+    """Once a layer is built, its weights may be overwritten or dropped on the current stream, although the context's own
+    stream has yet to read them."""
+    from post_quantization_expert_b200.pipeline import Fp4Layer
+    n, E, k, dm, dff = 40, 8, 2, 256, 256
+    w, X, lg = layer_case(n, E, k, dm, dff, 2, 128)
+    x, l = X.to(DEV), lg.to(DEV)
+    want = Fp4Layer(ctx, to_dev(w), k, n).forward(x, l, torch.empty((n, dm), device=DEV))
+    own = L.Context(0, torch.cuda.Stream())
+    Fp4Layer(own, to_dev(w), k, n)         # (leaves its buffers in the stream's pool: the next one is built without a wait)
+    mine = to_dev(w)
+    torch.cuda.synchronize()
+    with torch.cuda.stream(own.stream):    # some ten milliseconds
+        busy = torch.zeros((8192, 8192), dtype=BF16, device=DEV)
+        for _ in range(20):
+            busy = busy @ busy
+    layer = Fp4Layer(own, mine, k, n)
+    if how == "overwritten":
+        again = [t.fill_(7.0) for t in vars(mine).values()]
+    else:
+        sizes = [t.shape for t in vars(mine).values()]
+        del mine
+        again = [torch.full(s, 7.0, dtype=BF16, device=DEV) for s in sizes]
+    with torch.cuda.stream(own.stream):
+        got = layer.forward(x, l, torch.empty((n, dm), device=DEV))
+    torch.cuda.synchronize()
+    assert torch.equal(got, want) and all((t == 7.0).all() for t in again)
+    L.clha_check(own)
+    own.close()
