@@ -140,6 +140,16 @@ CLHA_API clha_status clha_gather_noalloc(clha_ctx* ctx, const void* X, clha_dtyp
                                          const int32_t* ids, int k, int E, void* X_packed, int64_t packed_rows,
                                          int64_t* seg, int32_t* perm);
 
+/* clha_gather with its scratch (the block histograms) in the caller's device memory instead of the
+ * context's workspace, which grows, and moves, whenever a call on the context needs more of it: a
+ * graph that captured this call keeps pointing at memory that the caller owns. perm is needed.
+ * scratch: 4-byte aligned, clha_gather_scratch_bytes(n, E) or more (-1 for a bad E or an n
+ * outside 0 .. 2^31 - 1; it grows with n); what it holds before and after does not matter. Nothing is allocated or synchronised. */
+CLHA_API int64_t clha_gather_scratch_bytes(int64_t n, int E);
+CLHA_API clha_status clha_gather_scratch(clha_ctx* ctx, const void* X, clha_dtype dtype, int64_t n, int d,
+                                         const int32_t* ids, int k, int E, void* X_packed, int64_t packed_rows,
+                                         int64_t* seg, int32_t* perm, void* scratch, int64_t scratch_bytes);
+
 /* Expert FFN activation feeding the down projection: h = SiLU(x Wg^T) * (x Wu^T) per token of
  * each expert, SiLU product in fp64, stored as bf16 (round to nearest even). The pages do not
  * spell this out: the down projection's Hessian needs its input, and that input is this product.
@@ -350,11 +360,12 @@ CLHA_API clha_status clha_loss(clha_ctx* ctx, const void* W, clha_dtype dtype, c
 /* ------------------------------------------------------------------------------ 4-bit expert layer */
 
 /* The layer that the quantized experts run in, in microscaled 4-bit floating point:
- *   clha_route_gated -> clha_gather (perm only) -> clha_fp4_quantize (the routed rows)
+ *   clha_route_gated -> clha_gather_scratch (perm only) -> clha_fp4_quantize (the routed rows)
  *   -> clha_fp4_expert_act -> clha_fp4_quantize -> clha_fp4_matmul -> clha_combine.
  * The pages stop at the quantized weights; these calls have no counterpart there. Nothing in them
  * synchronises, allocates or uses the context's workspace, so calls of several streams' contexts may
- * overlap and every call may be captured into a graph; results do not depend on timing. */
+ * overlap and every call may be captured into a graph; results do not depend on timing. (clha_gather
+ * gives the same perm and seg, but a graph that captured it is invalid once the workspace has grown.) */
 
 typedef enum { CLHA_SCORE_SOFTMAX = 0, CLHA_SCORE_SIGMOID = 1 } clha_score;
 typedef enum { CLHA_GROUP_MAX = 0, CLHA_GROUP_TOP2 = 1 } clha_group_rank;

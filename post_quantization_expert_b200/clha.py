@@ -30,6 +30,7 @@ ACT_AUTO, ACT_FMA, ACT_TENSOR = 0, 1, 2   # activation kernel policy (clha_set_a
 SYMBOLS = [
     "clha_create", "clha_destroy", "clha_last_error", "clha_check", "clha_version", "clha_kernel_launches",
     "clha_route_topk", "clha_packed_rows", "clha_gather", "clha_gather_noalloc", "clha_expert_act",
+    "clha_gather_scratch_bytes", "clha_gather_scratch",
     "clha_accum_create", "clha_accum_destroy", "clha_accum_zero", "clha_accum_buffers",
     "clha_accum_export", "clha_accum_import", "clha_collect",
     "clha_aggregate", "clha_factor", "clha_factor_groups", "clha_epmq_target", "clha_quantize", "clha_loss",
@@ -93,6 +94,8 @@ def load(path: str = LIB_PATH):
         "clha_packed_rows": (i64, [i64, i32, i32]),
         "clha_gather": (i32, [vp, vp, i32, i64, i32, vp, i32, i32, vp, i64, vp, vp]),
         "clha_gather_noalloc": (i32, [vp, vp, i32, i64, i32, vp, i32, i32, vp, i64, vp, vp]),
+        "clha_gather_scratch_bytes": (i64, [i64, i32]),
+        "clha_gather_scratch": (i32, [vp, vp, i32, i64, i32, vp, i32, i32, vp, i64, vp, vp, vp, i64]),
         "clha_expert_act": (i32, [vp, vp, i64, i32, vp, i32, vp, vp, i32, vp]),
         "clha_accum_create": (i32, [vp, i32, i32, i32, C.POINTER(vp)]),
         "clha_accum_destroy": (i32, [vp]),
@@ -219,6 +222,25 @@ def clha_gather_noalloc(ctx: Context, X, n: int, d: int, ids, k: int, E: int, X_
     """clha_gather with its scratch in the library's fixed device array (no allocation)."""
     ctx._check(load().clha_gather_noalloc(ctx.handle, _p(X), _dtype(X), n, d, _p(ids), k, E, _p(X_packed),
                                           packed_rows, _p(seg), _p(perm)))
+
+
+def clha_gather_scratch_bytes(n: int, E: int) -> int:
+    """Bytes of scratch that clha_gather_scratch needs for n tokens of E experts (-1 for a bad size)."""
+    return load().clha_gather_scratch_bytes(n, E)
+
+
+def clha_gather_scratch(ctx: Context, X, n: int, d: int, ids, k: int, E: int, X_packed, packed_rows: int, seg, perm,
+                        scratch):
+    """clha_gather with its scratch in the caller's tensor (uint8, clha_gather_scratch_bytes or more) instead of the
+    context's workspace."""
+    call, dev = "clha_gather_scratch", _device(ctx)
+    xp, xt = _float_arg(call, dev, "X", X, n * d)
+    ip = _arg(call, dev, "ids", ids, n * k, torch.int32)
+    pp = _arg(call, dev, "X_packed", X_packed, packed_rows * d, X.dtype)
+    sp, mp = _arg(call, dev, "seg", seg, 2 * E + 1, torch.int64), _arg(call, dev, "perm", perm, packed_rows, torch.int32)
+    cp = _arg(call, dev, "scratch", scratch, 0, torch.uint8)
+    ctx._check(load().clha_gather_scratch(ctx.handle, xp, xt, n, d, ip, k, E, pp, packed_rows, sp, mp, cp,
+                                          0 if scratch is None else scratch.numel()))
 
 
 def clha_expert_act(ctx: Context, X, rows: int, d_model: int, seg, E: int, Wg, Wu, d_ff: int, h):

@@ -200,27 +200,60 @@ extern "C" int64_t clha_packed_rows(int64_t n, int k, int E) {
 
 static int dtype_size(clha_dtype dt) { return dt == CLHA_BF16 ? 2 : (dt == CLHA_F32 ? 4 : 0); }
 
+// the checks that clha_gather and clha_gather_scratch share
+static clha_status gather_args(clha_ctx* ctx, const char* call, const void* X, clha_dtype dtype, int64_t n, int d,
+                               const int32_t* ids, int k, int E, void* X_packed, int64_t packed_rows, int64_t* seg,
+                               int32_t* perm) {
+    REQUIRE(dtype_size(dtype), CLHA_ERR_INVALID_ARG, "%s: unknown dtype", call);
+    REQUIRE(n >= 0 && d > 0, CLHA_ERR_INVALID_ARG, "%s: bad sizes", call);
+    REQUIRE(E >= 1 && E <= 1024 && k >= 1 && k <= E, CLHA_ERR_INVALID_ARG, "%s: need 1 <= k <= E <= 1024", call);
+    REQUIRE(d % 128 == 0, CLHA_ERR_UNSUPPORTED_SHAPE, "%s: d=%d is not a multiple of 128", call, d);
+    REQUIRE(packed_rows >= clha_packed_rows(n, k, E), CLHA_ERR_INVALID_ARG, "%s: packed_rows %lld < %lld", call,
+            (long long)packed_rows, (long long)clha_packed_rows(n, k, E));
+    REQUIRE(seg && (X_packed || perm) && (n == 0 || ids) && (!X_packed || n == 0 || X), CLHA_ERR_INVALID_ARG,
+            "%s: null pointer", call);
+    return CLHA_OK;
+}
+
 extern "C" clha_status clha_gather(clha_ctx* ctx, const void* X, clha_dtype dtype, int64_t n, int d,
                                    const int32_t* ids, int k, int E, void* X_packed, int64_t packed_rows,
                                    int64_t* seg, int32_t* perm) {
     CHECK_CTX(ctx);
-    int es = dtype_size(dtype);
-    REQUIRE(es, CLHA_ERR_INVALID_ARG, "clha_gather: unknown dtype");
-    REQUIRE(n >= 0 && d > 0, CLHA_ERR_INVALID_ARG, "clha_gather: bad sizes");
-    REQUIRE(E >= 1 && E <= 1024 && k >= 1 && k <= E, CLHA_ERR_INVALID_ARG, "clha_gather: need 1 <= k <= E <= 1024");
-    REQUIRE(d % 128 == 0, CLHA_ERR_UNSUPPORTED_SHAPE, "clha_gather: d=%d is not a multiple of 128", d);
-    REQUIRE(packed_rows >= clha_packed_rows(n, k, E), CLHA_ERR_INVALID_ARG,
-            "clha_gather: packed_rows %lld < %lld", (long long)packed_rows, (long long)clha_packed_rows(n, k, E));
-    REQUIRE(seg && (X_packed || perm) && (n == 0 || ids) && (!X_packed || n == 0 || X), CLHA_ERR_INVALID_ARG,
-            "clha_gather: null pointer");
+    clha_status st = gather_args(ctx, "clha_gather", X, dtype, n, d, ids, k, E, X_packed, packed_rows, seg, perm);
+    if (st) return st;
     SET_DEVICE(ctx);
     LaunchScope launch_scope(ctx);
     size_t wsb = gather_workspace_bytes(n, k, E, packed_rows);
     void* ws = nullptr;
-    clha_status st = clha_workspace(ctx, wsb, &ws);
+    st = clha_workspace(ctx, wsb, &ws);
     if (st) return st;
-    CUDA_TRY(launch_gather(ctx->stream, X, es, n, d, ids, k, E, X_packed, packed_rows, seg, perm, ws, wsb,
+    CUDA_TRY(launch_gather(ctx->stream, X, dtype_size(dtype), n, d, ids, k, E, X_packed, packed_rows, seg, perm, ws, wsb,
                            ctx->d_err), "clha_gather");
+    return CLHA_OK;
+}
+
+extern "C" int64_t clha_gather_scratch_bytes(int64_t n, int E) {
+    if (n < 0 || n >= (int64_t)1 << 31 || E < 1 || E > 1024) return -1;
+    const int64_t blocks = (n + kGatherBlockTokens - 1) / kGatherBlockTokens;
+    return (blocks < 1 ? 1 : blocks) * E * (int64_t)sizeof(int);
+}
+
+extern "C" clha_status clha_gather_scratch(clha_ctx* ctx, const void* X, clha_dtype dtype, int64_t n, int d,
+                                           const int32_t* ids, int k, int E, void* X_packed, int64_t packed_rows,
+                                           int64_t* seg, int32_t* perm, void* scratch, int64_t scratch_bytes) {
+    CHECK_CTX(ctx);
+    clha_status st = gather_args(ctx, "clha_gather_scratch", X, dtype, n, d, ids, k, E, X_packed, packed_rows, seg, perm);
+    if (st) return st;
+    REQUIRE(perm && scratch && ((uintptr_t)scratch & 3) == 0, CLHA_ERR_INVALID_ARG,
+            "clha_gather_scratch: perm and scratch (4-byte aligned) are needed");
+    const int64_t need = clha_gather_scratch_bytes(n, E);
+    REQUIRE(need >= 0 && scratch_bytes >= need, CLHA_ERR_INVALID_ARG,
+            "clha_gather_scratch: %lld bytes of scratch, needs %lld (-1: 2^31 tokens or more)", (long long)scratch_bytes,
+            (long long)need);
+    SET_DEVICE(ctx);
+    LaunchScope launch_scope(ctx);
+    CUDA_TRY(launch_gather(ctx->stream, X, dtype_size(dtype), n, d, ids, k, E, X_packed, packed_rows, seg, perm, scratch,
+                           (size_t)scratch_bytes, ctx->d_err), "clha_gather_scratch");
     return CLHA_OK;
 }
 

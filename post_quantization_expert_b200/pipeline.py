@@ -10,8 +10,8 @@ This module only orders calls and owns device buffers; every step runs in libclh
 Always-active shared experts see every token: their gate/up input Hessian is one slot shared by
 all of them, and they are quantized with one more bit (CLHA-MP).
 Fp4Layer runs a layer whose experts are in microscaled 4-bit floating point:
-  clha_route_gated -> clha_gather (permutation) -> clha_fp4_quantize -> clha_fp4_expert_act -> clha_fp4_quantize
-  -> clha_fp4_matmul -> clha_combine
+  clha_route_gated -> clha_gather_scratch (permutation) -> clha_fp4_quantize -> clha_fp4_expert_act
+  -> clha_fp4_quantize -> clha_fp4_matmul -> clha_combine
 """
 from __future__ import annotations
 
@@ -633,12 +633,14 @@ class EPMQCalibration:
 class Fp4Layer:
     """One MoE layer that runs its experts in microscaled 4-bit floating point. The weights are quantized once,
     at construction (round to nearest; the blocks' scales are all the calibration they need); forward() then is
-      clha_route_gated -> clha_gather (the permutation) -> clha_fp4_quantize (the routed rows)
+      clha_route_gated -> clha_gather_scratch (the permutation) -> clha_fp4_quantize (the routed rows)
       -> clha_fp4_expert_act -> clha_fp4_quantize -> clha_fp4_matmul -> clha_combine.
     Always-active experts see every token with weight 1: their gate, up and down projections are laid side by
-    side, so that they run as one dense expert whose output is the combination's addend. Buffers are the
-    layer's own; forward() queues work on the context's stream and synchronises nothing, and after one
-    eager call (which sizes the gather's workspace) it can be captured into a graph."""
+    side, so that they run as one dense expert whose output is the combination's addend. Buffers, the
+    gather's scratch among them, are the layer's own and keep their place: forward() queues work on the
+    context's stream, allocates and synchronises nothing, and can be captured into a graph, which stays
+    valid as long as the layer lives, whatever else runs on the context. One layer's calls and graphs
+    share its buffers, so they run one after the other."""
 
     def __init__(self, ctx: L.Context, w: MoEWeights, k: int, max_tokens: int, fmt: int = L.FP4_E4M3_16,
                  score: int = L.SCORE_SOFTMAX, bias: torch.Tensor | None = None, n_groups: int = 1, top_groups: int = 1,
@@ -675,6 +677,7 @@ class Fp4Layer:
         self.counts = torch.empty(E, dtype=torch.int32, device=dev)
         self.seg = torch.empty(2 * E + 1, dtype=torch.int64, device=dev)
         self.perm = torch.empty(self.P, dtype=torch.int32, device=dev)
+        self.scratch = torch.empty(L.clha_gather_scratch_bytes(max_tokens, E), dtype=torch.uint8, device=dev)
         self.x = self._operand(self.P, dm)
         self.h = torch.empty((self.P, dff), dtype=torch.bfloat16, device=dev)
         self.hq = self._operand(self.P, dff)
@@ -717,7 +720,7 @@ class Fp4Layer:
         ids, weights = self.ids[:n], self.weights[:n]
         with t.span("route"):
             L.clha_route_gated(ctx, logits, n, E, k, ids, weights, self.counts, **self.gate)
-            L.clha_gather(ctx, X, n, dm, ids, k, E, None, P, self.seg, self.perm)
+            L.clha_gather_scratch(ctx, X, n, dm, ids, k, E, None, P, self.seg, self.perm, self.scratch)
         seg = dict(seg=self.seg, E=E)
         with t.span("quantize"):
             L.clha_fp4_quantize(ctx, X, n, dm, fmt, *self.x, tensor_scale=xs, perm=self.perm, rows=P, **seg)

@@ -836,3 +836,60 @@ def test_layer_weights_are_the_callers_again(ctx, how):
     assert torch.equal(got, want) and all((t == 7.0).all() for t in again)
     L.clha_check(own)
     own.close()
+
+
+@pytest.mark.parametrize("n,E,k", [(0, 4, 2), (1, 64, 6), (300, 10, 3), (1000, 300, 4)])
+def test_gather_with_the_callers_scratch(ctx, n, E, k):
+    """The same permutation, segments and rows as clha_gather, within the bytes that it asks for; fewer are refused."""
+    ids = torch.from_numpy(route(n, E, k, n)[0]).to(DEV)
+    X = torch.randn((n, 128), generator=gen(n)).to(DEV)
+    P, need = L.clha_packed_rows(n, k, E), L.clha_gather_scratch_bytes(n, E)
+
+    def run(call, *scratch):
+        perm, seg = torch.zeros(P, dtype=torch.int32, device=DEV), torch.zeros(2 * E + 1, dtype=torch.int64, device=DEV)
+        out = torch.full((P, 128), 5.0, device=DEV)
+        call(ctx, X, n, 128, ids, k, E, out, P, seg, perm, *scratch)
+        return perm, seg, out
+    buf = torch.full((need + 256,), 0xA5, dtype=torch.uint8, device=DEV)
+    for a, b in zip(run(L.clha_gather), run(L.clha_gather_scratch, buf[:need])):
+        assert torch.equal(a, b)
+    assert (buf[need:] == 0xA5).all()
+    for bad in (buf[:need - 1], buf[1:], None):
+        with pytest.raises(L.ClhaError):
+            run(L.clha_gather_scratch, bad)
+    L.clha_check(ctx)
+
+
+def test_layer_graph_outlives_the_workspace():
+    """A forward captured before any eager call, replayed after calls that make the context's workspace grow and move."""
+    from post_quantization_expert_b200.pipeline import Fp4Layer
+    n, E, k, dm, dff = 600, 8, 2, 256, 256
+    w, X, lg = layer_case(n, E, k, dm, dff, 1, 128)
+    x, l = X.to(DEV), lg.to(DEV)
+    s = torch.cuda.Stream()
+    own = L.Context(0, s)
+    layer = Fp4Layer(own, to_dev(w), k, n)
+    few, some = torch.zeros((3, dm), device=DEV), torch.zeros((n, dm), device=DEV)
+    torch.cuda.synchronize()
+    small, large = torch.cuda.CUDAGraph(), torch.cuda.CUDAGraph()
+    with torch.cuda.graph(small, stream=s):
+        layer.forward(x[:3], l[:3], few)
+    with torch.cuda.graph(large, stream=s):
+        layer.forward(x, l, some)
+    with torch.cuda.stream(s):
+        want = layer.forward(x, l, torch.empty((n, dm), device=DEV))
+        ids = torch.zeros((1 << 20, 1), dtype=torch.int32, device=DEV)
+        P = L.clha_packed_rows(1 << 20, 1, 64)
+        for _ in range(2):
+            L.clha_gather(own, torch.empty((1 << 20, 128), device=DEV), 1 << 20, 128, ids, 1, 64, None, P,
+                          torch.empty(129, dtype=torch.int64, device=DEV), torch.empty(P, dtype=torch.int32, device=DEV))
+        for _ in range(3):
+            large.replay()
+            small.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(some, want)
+    with torch.cuda.stream(s):
+        assert torch.equal(few, layer.forward(x[:3], l[:3], torch.empty_like(few)))
+    L.clha_check(own)
+    del small, large
+    own.close()

@@ -92,3 +92,26 @@ def test_null_context(lib):
     assert lib.clha_fp4_matmul(n, 0, n, n, n, 0, 128, n, 1, n, n, n, 128, n, 0) == L.ERR_INVALID_ARG
     assert lib.clha_fp4_expert_act(n, 0, n, n, n, 0, 128, n, 1, n, n, n, n, n, n, 128, n) == L.ERR_INVALID_ARG
     assert lib.clha_combine(n, n, 0, 0, 128, n, n, 0, 1, 1, n, n, n, 0, n, 0) == L.ERR_INVALID_ARG
+
+
+def test_gather_scratch():
+    assert L.clha_gather_scratch_bytes(0, 8) == 8 * 4
+    assert L.clha_gather_scratch_bytes(256, 64) == 64 * 4
+    assert L.clha_gather_scratch_bytes(257, 64) == 2 * 64 * 4
+    for bad in ((-1, 8), (1, 0), (1, 1025), (2 ** 31, 8)):
+        assert L.clha_gather_scratch_bytes(*bad) == -1
+    ok = dict(X=t(4, 128), ids=t(4, 1, dtype=I32), X_packed=None, seg=t(3, dtype=I64), perm=t(132, dtype=I32),
+              scratch=t(4, dtype=U8))
+
+    def call(**kw):
+        a = {**ok, **kw}
+        L.clha_gather_scratch(None, a["X"], 4, 128, a["ids"], 1, 1, a["X_packed"], 132, a["seg"], a["perm"], a["scratch"])
+    for kw in (dict(X=t(4, 127)), dict(ids=t(3, 1, dtype=I32)), dict(X_packed=t(131, 128)), dict(seg=t(2, dtype=I64)),
+               dict(perm=t(131, dtype=I32))):
+        with pytest.raises(ValueError, match=next(iter(kw))):
+            call(**kw)
+    for kw in (dict(scratch=t(4)), dict(X_packed=t(132, 128, dtype=BF16))):
+        with pytest.raises(TypeError, match=next(iter(kw))):
+            call(**kw)
+    n = None
+    assert L.load().clha_gather_scratch(n, n, 0, 0, 128, n, 1, 1, n, 128, n, n, n, 0) == L.ERR_INVALID_ARG
