@@ -400,9 +400,10 @@ cudaError_t launch_q(cudaStream_t s, int num_sms, const QuantArgs& p) {
 }
 
 // ------------------------------------------------------------------------------ decoding
-// q s g rounded once: q s is exact (6 bits) and float32's product with g is one rounding. A bfloat16 result
-// rounds the product towards zero first and keeps a sticky bit, so that it too is rounded once (without g it is
-// exact).
+// q s g rounded once: q s is exact (6 bits) and float32's product with g is one rounding. Under the two largest
+// power-of-two scales q s may pass float32's range where q s g does not: a quarter of s then meets four times g,
+// both exact (for |g| >= 1 the value overflows with q s). A bfloat16 result rounds the product towards zero first and
+// keeps a sticky bit, so that it too is rounded once (without g it is exact).
 __device__ __forceinline__ float sticky(float v, float g) {
     const float t = __fmul_rz(v, g);
     return __fmaf_rn(v, g, -t) != 0.f ? __uint_as_float(__float_as_uint(t) | 1u) : t;
@@ -446,7 +447,11 @@ __global__ void __launch_bounds__(kThreads) fp4_dequantize_kernel(const uint8_t*
                 s = byte == 0xff ? NAN : pow2_byte(byte);
             else
                 s = byte == 0x7f ? NAN : from_e4m3(byte & 0x7f);
-            const float gr = SCALED ? __ldg(g + row / rows_per_g) : 1.f;
+            float gr = SCALED ? __ldg(g + row / rows_per_g) : 1.f;
+            if (BLOCK == 32 && SCALED && byte >= 253 && byte != 0xff && fabsf(gr) < 1.f) {
+                s *= 0.25f;
+                gr *= 4.f;
+            }
             float v[16];
 #pragma unroll
             for (int h = 0; h < 2; ++h) {

@@ -893,3 +893,27 @@ def test_layer_graph_outlives_the_workspace():
     L.clha_check(own)
     del small, large
     own.close()
+
+
+def every_scale(ctx, fmt, g):
+    """Every code under every finite scale byte, one row for each of the matrix scales g (host float32): the codes and
+    tiled scales on the device, and their exact values."""
+    top = 255 if fmt == "e8m0_32" else 127
+    byte = np.tile(np.minimum(np.arange((top + 7) // 8 * 8), top - 1).astype(np.uint8), (len(g), 1))
+    codes = np.tile(np.arange(16, dtype=np.uint8), (len(g), byte.shape[1] * O.BLOCK[fmt] // 16))
+    want = O.fp4_values(codes, byte, fmt, to64(g))
+    return torch.from_numpy(O.pack_codes4(codes)).to(DEV), torch.from_numpy(O.tile_scales(byte)).to(DEV), want
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+def test_dequantize_every_scale(ctx, fmt):
+    """float32 values of every code and finite scale, rounded once, also where q * s alone passes float32's range."""
+    g = torch.tensor([1.0, 0.37, 2.0 ** -20, 1.0 - 2.0 ** -24, 1.0 + 2.0 ** -23, 3.3e-12, 1.3 * 2.0 ** -100, 2.0 ** -126, 1e-42,
+                      1e30, 3e38])
+    codes, scales, want = every_scale(ctx, fmt, g)
+    with np.errstate(over="ignore"):
+        want32 = want.astype(np.float32)
+    got = torch.empty(want.shape, device=DEV)
+    L.clha_fp4_dequantize(ctx, codes, scales, *want.shape, FMT[fmt], got, tensor_scale=g.to(DEV))
+    np.testing.assert_array_equal(got.cpu().numpy(), want32)
+    L.clha_check(ctx)
