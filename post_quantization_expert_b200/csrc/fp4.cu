@@ -403,10 +403,17 @@ cudaError_t launch_q(cudaStream_t s, int num_sms, const QuantArgs& p) {
 // q s g rounded once: q s is exact (6 bits) and float32's product with g is one rounding. Under the two largest
 // power-of-two scales q s may pass float32's range where q s g does not: a quarter of s then meets four times g,
 // both exact (for |g| >= 1 the value overflows with q s). A bfloat16 result rounds the product towards zero first and
-// keeps a sticky bit, so that it too is rounded once (without g it is exact).
+// keeps a sticky bit, so that it too is rounded once (without g it is exact). What the rounding towards zero cut off
+// may lie below 2^-149, float32's smallest number, where the product is below 2^-120: it is looked at 2^64 times as
+// large there. (A product cut off to zero is zero in bfloat16 too.)
 __device__ __forceinline__ float sticky(float v, float g) {
     const float t = __fmul_rz(v, g);
-    return __fmaf_rn(v, g, -t) != 0.f ? __uint_as_float(__float_as_uint(t) | 1u) : t;
+    float u = t;
+    if (fabsf(t) < 0x1p-100f && t != 0.f) {
+        u *= 0x1p64f;
+        if (fabsf(v) > 1.f) g *= 0x1p64f; else v *= 0x1p64f;   // |v| > 1: |g| < 2^-100
+    }
+    return __fmaf_rn(v, g, -u) != 0.f ? __uint_as_float(__float_as_uint(t) | 1u) : t;
 }
 __device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
     uint32_t r;

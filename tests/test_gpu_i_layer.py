@@ -917,3 +917,32 @@ def test_dequantize_every_scale(ctx, fmt):
     L.clha_fp4_dequantize(ctx, codes, scales, *want.shape, FMT[fmt], got, tensor_scale=g.to(DEV))
     np.testing.assert_array_equal(got.cpu().numpy(), want32)
     L.clha_check(ctx)
+
+
+def nearest_bf16(x64):
+    """Float64 -> bf16, nearest even, in one rounding, subnormal numbers included."""
+    step = np.ldexp(1.0, np.maximum(np.frexp(x64)[1], -125) - 8)
+    return torch.from_numpy(np.rint(x64 / step) * step).to(BF16)
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+def test_dequantize_small_values_to_bf16(ctx, fmt):
+    """Values above the middle between two bf16 numbers by less than float32 can hold there: v G = T 2^shift + r with T odd
+    of 9 bits, v = 3 or 27 and 0 < r < v, times a power of two. Rounded once, they go up."""
+    if fmt == "e4m3_16":
+        v, unit, code, byte, shift = 27, -10, 3, O.E4M3.tolist().index(9 * 2.0 ** -9), 20     # q s = 1.5 * 9 * 2^-9
+    else:
+        v, unit, code, byte, shift = 3, -21, 3, 127 - 20, 17                                  # q s = 1.5 * 2^-20
+    T = np.arange(257, 512, 2, dtype=np.int64) << shift
+    G = T // v + 1
+    G = G[(G < 2 ** 24) & (G * v > T)]
+    for low in (-126, -130, -122, 0):                                                         # T 2^-shift 2^(low - 8) >= 2^low
+        g = torch.from_numpy(np.ldexp(G.astype(np.float64), low - 8 - shift - unit)).float()
+        codes = np.full((len(g), 128), code, np.uint8)
+        bytes_ = np.full((len(g), 128 // O.BLOCK[fmt]), byte, np.uint8)
+        want = nearest_bf16(O.fp4_values(codes, bytes_, fmt, to64(g)))
+        got = torch.empty((len(g), 128), dtype=BF16, device=DEV)
+        L.clha_fp4_dequantize(ctx, torch.from_numpy(O.pack_codes4(codes)).to(DEV), torch.from_numpy(O.tile_scales(bytes_)).to(DEV),
+                              len(g), 128, FMT[fmt], got, tensor_scale=g.to(DEV))
+        assert torch.equal(got.cpu(), want), low
+    L.clha_check(ctx)
