@@ -71,7 +71,17 @@ struct MatmulArgs {
     int* err;
 };
 
-__device__ __forceinline__ float silu_mul(float g, float u) { return __fdividef(g, 1.f + __expf(-g)) * u; }
+// SiLU(g) u = g / (1 + e^-g) u. With h = e^(-|g| / 2) it is g / (1 + h h) u, and g h / (1 + h h) (u h) for g < 0: nothing
+// overflows or is flushed before |g| = 174, where h h u is below float32's range for any u. (1 + e^-g itself passes 2^126 at
+// g = -87.4, and the fast division by more than that gives 0, while u may bring the value back.) Off by at most
+// (1.5 |g| + 16) 2^-24 of its size: the exponent is rounded twice, h by two steps, six operations follow.
+__device__ __forceinline__ float silu_mul(float g, float u) {
+    float h, r;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(h) : "f"(fabsf(g) * -0.72134752f));   // log2(e) / 2
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(fmaf(h, h, 1.f)));
+    const float m = g < 0.f ? h : 1.f;
+    return g * m * r * (u * m);
+}
 
 template <typename OUT>
 __device__ __forceinline__ void store4(OUT* y, float a, float b, float c, float d);

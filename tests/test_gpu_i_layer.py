@@ -946,3 +946,32 @@ def test_dequantize_small_values_to_bf16(ctx, fmt):
                               len(g), 128, FMT[fmt], got, tensor_scale=g.to(DEV))
         assert torch.equal(got.cpu(), want), low
     L.clha_check(ctx)
+
+
+def act_between(h, g, u):
+    """h against silu(g) u of exact sums g, u (float64), rounded once to bf16. The exponential's argument is rounded twice (its
+    constant and the product), 1.5 2^-24 |g|; the exponential of its half is off by 2^-22 and counts twice, the reciprocal by
+    2^-23, six more operations by 2^-24 each."""
+    d = (1.5 * np.abs(g) + 16) * 2.0 ** -24
+    want = O.silu(g) * u
+    a, b = (round_bf16(want * (1 + s * d)) for s in (-1, 1))
+    return bool(((h.cpu() >= torch.minimum(a, b)) & (h.cpu() <= torch.maximum(a, b))).all())
+
+
+@pytest.mark.parametrize("sign", [-1, 1])
+@pytest.mark.parametrize("n,K,N", [(20, 128, 128), (64, 128, 256), (3, 4096, 128), (4000, 128, 1024)])
+def test_act_of_large_sums(ctx, sign, n, K, N):
+    """Gate sums from +-1 to +-92 that are exact (one product of two values each), beside up sums large enough that silu's
+    smallest values count."""
+    x, w, u = torch.zeros((n, K)), torch.zeros((N, K)), torch.zeros((N, K))
+    x[:, 0] = sign * torch.linspace(1, 9.6, n)
+    x[:, 64] = 1.0
+    w[:, 0] = torch.linspace(1, 9.6, N)
+    u[:, 64] = torch.tensor([1.0, -3.0]).repeat(N // 2)
+    (xq, xs, x64), (wq, ws, w64), (uq, us, u64) = (operand(ctx, t, "e4m3_16") for t in (x, w, u))
+    h = torch.empty((n, N), dtype=BF16, device=DEV)
+    big = torch.tensor([2.0 ** 100], device=DEV)
+    L.clha_fp4_expert_act(ctx, L.FP4_E4M3_16, xq, xs, n, K, wq, ws, uq, us, N, h, u_scale=big)
+    g = x64 @ w64.T
+    assert np.abs(g).max() > 91 and act_between(h, g, x64 @ u64.T * 2.0 ** 100)
+    L.clha_check(ctx)
