@@ -77,7 +77,8 @@ __device__ __forceinline__ void warp_best(F& v, int& i) {
     }
 }
 
-// Bound on the difference of two float32 choices whose exact order it leaves open. A sigmoid, 1 / (1 + e), is off by
+// Bound on the difference of two float32 choices whose exact order it leaves open. A sigmoid, 1 / (1 + e) or, for l < 0,
+// e / (1 + e) with e = e^-|l| (1 + e^-l passes 2^126 at l = -87.4, and the fast division by more than that gives 0), is off by
 // less than 2^-24 through e (two steps, 2^-22 of it, times s (1 - s) <= 1/4), 2^-24 through the sum and 2^-22 through
 // the fast division (two steps): 1.5 2^-22. A softmax is off by less than 2^-18 of the largest score: 2^-22 and the
 // rounded argument's 0.37 2^-24 through the exponential, as much through the sum, whose up to 37 roundings add
@@ -120,7 +121,10 @@ __device__ __forceinline__ bool select_token(const GateArgs& p, const float (&l)
         top_score = 1 / sum;
     } else {
 #pragma unroll
-        for (int i = 0; i < VPL; ++i) s[i] = lane + 32 * i < p.E ? 1 / (1 + expf(-l[i])) : 0;
+        for (int i = 0; i < VPL; ++i) {
+            const float e = expf(-fabsf(l[i]));
+            s[i] = lane + 32 * i < p.E ? (l[i] < 0 ? e : 1) / (1 + e) : 0;
+        }
     }
     unsigned live = 0;   // bit i: expert lane + 32 i may be chosen
 #pragma unroll
@@ -498,7 +502,9 @@ __global__ void __launch_bounds__(kWarps * 32, VPL == 8 ? 4 : 2) route_lanes_ker
             top_score = 1.f / lanes_sum<LPT>(sum);
         }
         const auto score = [&](float l) {
-            return p.sigmoid ? __fdividef(1.f, 1.f + expf(-l)) : expf(l - m) * top_score;
+            if (!p.sigmoid) return expf(l - m) * top_score;
+            const float e = expf(-fabsf(l));
+            return __fdividef(l < 0.f ? e : 1.f, 1.f + e);
         };
         const float slack = choice_slack(p.sigmoid != 0, top_score);
         if (!by_logit) {

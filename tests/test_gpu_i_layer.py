@@ -975,3 +975,20 @@ def test_act_of_large_sums(ctx, sign, n, K, N):
     g = x64 @ w64.T
     assert np.abs(g).max() > 91 and act_between(h, g, x64 @ u64.T * 2.0 ** 100)
     L.clha_check(ctx)
+
+
+@pytest.mark.parametrize("E", [30, 64, 256, 500, 600])
+def test_route_small_sigmoid_scores(ctx, E):
+    """Sigmoids at the lower end of float32, as weights times a scale that brings them back. The exponential and the
+    division are off by 2^-22 each, or by two steps of 2^-149 where they are subnormal, the scaling by 2^-24."""
+    k, scale = 8, 2.0 ** 100
+    l, bias = -80 - 20 * torch.rand((40, E), generator=gen(E)), torch.linspace(0, 1, E)
+    ids, w, counts = (torch.empty((40, k), dtype=torch.int32, device=DEV), torch.empty((40, k), device=DEV),
+                      torch.empty(E, dtype=torch.int32, device=DEV))
+    L.clha_route_gated(ctx, l.to(DEV), 40, E, k, ids, w, counts, score=L.SCORE_SIGMOID, renormalise=False, scale=scale,
+                       bias=bias.to(DEV))
+    want_ids, want, _ = O.route_gated(to64(l), k, score="sigmoid", renormalise=False, scale=scale, bias=to64(bias))
+    got = to64(w)
+    np.testing.assert_array_equal(ids.cpu().numpy(), want_ids)
+    assert (np.abs(got - want) <= 2.0 ** -20 * want + 4 * 2.0 ** -149 * scale).all(), float((got / want).min())
+    L.clha_check(ctx)
