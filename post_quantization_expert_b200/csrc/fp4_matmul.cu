@@ -26,6 +26,8 @@
 #include "tc_ptx.h"
 #include "tmap.h"
 
+#include <cfloat>
+
 namespace {
 
 constexpr int kThreads = 320;
@@ -106,6 +108,30 @@ __device__ __forceinline__ float4 ld_cluster_f4(uint32_t addr) {
                  : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(addr) : "memory");
     return v;
 }
+
+// What the finished sums are multiplied by, first `pre`, then `by`: the product of X's and W's matrix scales, rounded once.
+// pre is 1 unless that product leaves float32's normal range, where the scaled sums may well be inside it: pre takes half
+// of its exponent then, so that neither step overflows or is flushed before the result is. Two sums an instruction, so
+// that the second step costs no more than one step on single sums does.
+struct MatrixScale {
+    float pre, by;
+    __device__ __forceinline__ MatrixScale(float x, float w) : pre(1.f), by(x * w) {
+        if (fabsf(by) >= 0x1p-126f && fabsf(by) < INFINITY) return;
+        const double p = (double)x * (double)w;
+        if (!(fabs(p) < 0x1p256)) return;                          // (an Inf or NaN scale)
+        const int h = max(-126, min(127, ((__double2hiint(p) >> 20 & 0x7ff) - 1023) / 2));
+        pre = __int_as_float((h + 127) << 23);
+        by = fmaxf(-FLT_MAX, fminf(FLT_MAX, (float)(p * __hiloint2double((1023 - h) << 20, 0))));
+    }
+    template <int N>
+    __device__ __forceinline__ void apply(uint32_t (&v)[N]) const {
+#pragma unroll
+        for (int i = 0; i < N; i += 2)
+            asm("{\n\t.reg .b64 a, b, c;\n\tmov.b64 a, {%0, %1};\n\tmov.b64 b, {%2, %2};\n\tmov.b64 c, {%3, %3};\n\t"
+                "mul.rn.f32x2 a, a, b;\n\tmul.rn.f32x2 a, a, c;\n\tmov.b64 {%0, %1}, a;\n\t}"
+                : "+r"(v[i]), "+r"(v[i + 1]) : "f"(pre), "f"(by));
+    }
+};
 
 // ------------------------------------------------------------------------------ few rows
 struct Tile {
@@ -272,8 +298,7 @@ fp4_matmul_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant
         for (int64_t w = w0; w < total; w += stride, ++tcount) {
             const Tile t = tile(w);
             const int acc = tcount % C::ACCS;
-            const float ag = xg * (p.wg ? __ldg(p.wg + t.e) : 1.f);
-            const float au = ACT ? xg * (p.ug ? __ldg(p.ug + t.e) : 1.f) : 0.f;
+            const MatrixScale ag(xg, p.wg ? __ldg(p.wg + t.e) : 1.f), au(xg, ACT && p.ug ? __ldg(p.ug + t.e) : 1.f);
             if (!tc::mbar_wait_bounded(tfull0 + 8 * acc, (tcount / C::ACCS) & 1, abort_flag)) break;
             tc::fence_after_sync();
             const uint32_t tb = tmem + acc * (NB * XR) + ((uint32_t)(q * 32) << 16);
@@ -292,12 +317,14 @@ fp4_matmul_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant
                                 part[(x * XR + r0 + j) * 128 + col] = __uint_as_float(v[x][j]);
                     continue;
                 }
+                ag.apply(v[0]);
+                if (ACT) au.apply(v[NB - 1]);
                 OUT* y = Y + (t.m0 + r0) * p.N + t.n0 + col;
 #pragma unroll
                 for (int j = 0; j < 32; ++j)
                     if (r0 + j < t.tokens) {
-                        const float a = __uint_as_float(v[0][j]) * ag;
-                        store1(y + (int64_t)j * p.N, ACT ? silu_mul(a, __uint_as_float(v[NB - 1][j]) * au) : a);
+                        const float a = __uint_as_float(v[0][j]);
+                        store1(y + (int64_t)j * p.N, ACT ? silu_mul(a, __uint_as_float(v[NB - 1][j])) : a);
                     }
             }
             tc::fence_before_sync();
@@ -321,8 +348,7 @@ fp4_matmul_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant
         if (w0 < total && !*abort_flag) {
             const Tile t = tile(w0);
             const float xg = p.xg ? __ldg(p.xg) : 1.f;
-            const float ag = xg * (p.wg ? __ldg(p.wg + t.e) : 1.f);
-            const float au = ACT ? xg * (p.ug ? __ldg(p.ug + t.e) : 1.f) : 0.f;
+            const MatrixScale ag(xg, p.wg ? __ldg(p.wg + t.e) : 1.f), au(xg, ACT && p.ug ? __ldg(p.ug + t.e) : 1.f);
             const int groups = 32 / S;                             // 4-column groups of this CTA
             const uint32_t part = tc::smem_u32(smem);
             OUT* Y = reinterpret_cast<OUT*>(p.Y);
@@ -340,7 +366,10 @@ fp4_matmul_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant
                         }
                     }
 #pragma unroll
-                    for (int x = 0; x < 4; ++x) a[x] = ACT ? silu_mul(a[x] * ag, u[x] * au) : a[x] * ag;
+                    for (int x = 0; x < 4; ++x) {
+                        a[x] = a[x] * ag.pre * ag.by;
+                        if (ACT) a[x] = silu_mul(a[x], u[x] * au.pre * au.by);
+                    }
                 }
                 store4<OUT>(Y + (t.m0 + r) * p.N + t.n0 + c4 * 4, a[0], a[1], a[2], a[3]);
             }
@@ -557,8 +586,7 @@ fp4_matmul_pair_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_con
             const int64_t r0 = m0 + (int)rank * 128 + q * 32;          // this warp's first row
             const int64_t vend = p.seg ? p.seg[k.e] + p.seg[p.E + 1 + k.e] : p.rows;
             const bool real = r0 + lane < vend;
-            const float ag = xg * (p.wg ? __ldg(p.wg + k.e) : 1.f);
-            const float au = ACT ? xg * (p.ug ? __ldg(p.ug + k.e) : 1.f) : 0.f;
+            const MatrixScale ag(xg, p.wg ? __ldg(p.wg + k.e) : 1.f), au(xg, ACT && p.ug ? __ldg(p.ug + k.e) : 1.f);
             if (!tc::mbar_wait_bounded(tfull, tcount & 1, abort_flag)) break;
             tc::fence_after_sync();
             const uint32_t tb = tmem + ((uint32_t)(q * 32) << 16);
@@ -576,6 +604,8 @@ fp4_matmul_pair_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_con
             constexpr int BOXES = (ACT ? 64 : 128) / PER;
 #pragma unroll
             for (int b = 0; b < BOXES; ++b) {
+#pragma unroll
+                for (int i = 0; i < 4 / BOXES; ++i) (ACT && i >= 2 ? au : ag).apply(v[b * (4 / BOXES) + i]);
                 if (lane == 0) tc::bulk_wait_read<0>();                // the buffer's last store has read it
                 __syncwarp();
 #pragma unroll
@@ -584,7 +614,7 @@ fp4_matmul_pair_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_con
                     if (sizeof(OUT) == 4) {
 #pragma unroll
                         for (int x = 0; x < 4; ++x)
-                            o[x] = real ? __float_as_uint(__uint_as_float(v[b][4 * j + x]) * ag) : 0u;
+                            o[x] = real ? v[b][4 * j + x] : 0u;
                     } else {
 #pragma unroll
                         for (int x = 0; x < 4; ++x) {
@@ -592,8 +622,8 @@ fp4_matmul_pair_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_con
                             float f[2];
 #pragma unroll
                             for (int y = 0; y < 2; ++y) {
-                                f[y] = __uint_as_float(v[(c + y) >> 5][(c + y) & 31]) * ag;
-                                if (ACT) f[y] = silu_mul(f[y], __uint_as_float(v[(((c + y) >> 5) + 2) & 3][(c + y) & 31]) * au);
+                                f[y] = __uint_as_float(v[(c + y) >> 5][(c + y) & 31]);
+                                if (ACT) f[y] = silu_mul(f[y], __uint_as_float(v[(((c + y) >> 5) + 2) & 3][(c + y) & 31]));
                             }
                             o[x] = real ? pack_bf16(f[0], f[1]) : 0u;
                         }

@@ -992,3 +992,26 @@ def test_route_small_sigmoid_scores(ctx, E):
     np.testing.assert_array_equal(ids.cpu().numpy(), want_ids)
     assert (np.abs(got - want) <= 2.0 ** -20 * want + 4 * 2.0 ** -149 * scale).all(), float((got / want).min())
     L.clha_check(ctx)
+
+
+@pytest.mark.parametrize("x_scale,w_scale,top", [(1.3 * 2.0 ** -70, 1.7 * 2.0 ** -72, 40), (2.0 ** 100, 1.5 * 2.0 ** 40, -60),
+                                                 (3e-39, 1.0, 10), (1e-20, 1e30, 3)])
+def test_products_under_extreme_matrix_scales(ctx, x_scale, w_scale, top):
+    """Matrix scales whose product leaves float32's (normal) range while the scaled sums do not: rows of zeros stay zero,
+    and the sums keep their bits. Values around 2^top."""
+    for n, K, N in ((20, 256, 128), (3, 4096, 128), (64, 256, 256), (4000, 256, 1024)):
+        x, w = (torch.randn((r, K), generator=gen(r)) * 2.0 ** top for r in (n, N))
+        x[2] = 0
+        (xq, xs, x64), (wq, ws, w64) = operand(ctx, x, "e8m0_32"), operand(ctx, w, "e8m0_32")
+        a, b = (torch.tensor([v], device=DEV) for v in (x_scale, w_scale))
+        both = float(np.float64(np.float32(x_scale)) * np.float64(np.float32(w_scale)))
+        for out in (F32, BF16):
+            y = torch.empty((n, N), dtype=out, device=DEV)
+            L.clha_fp4_matmul(ctx, L.FP4_E8M0_32, xq, xs, n, K, wq, ws, N, y, x_scale=a, w_scale=b)
+            check_product(y, x64 @ w64.T * both, np.abs(x64) @ np.abs(w64).T * both, K, out)
+            assert (y[2] == 0).all()
+        h = torch.empty((n, N), dtype=BF16, device=DEV)
+        L.clha_fp4_expert_act(ctx, L.FP4_E8M0_32, xq, xs, n, K, wq, ws, wq, ws, N, h, x_scale=a, g_scale=b, u_scale=b)
+        check_act(h, x64 * both, w64[None], w64[None], None, K)
+        assert (h[2] == 0).all()
+    L.clha_check(ctx)
