@@ -649,9 +649,17 @@ class Fp4Layer:
         """w: the layer's weights (bf16 or f32). bias, n_groups, ... scale: as clha_route_gated takes them. x_scale,
         h_scale (float32 [1] on the device): matrix scales of the layer's input and of the experts' activations, for
         values that e4m3 block scales alone do not reach (above 2688, or around 2^-9 and below); none by default."""
+        E, dm, dff = w.Wd.shape
+        ns, sdff = (w.Sgu.shape[0] // 2, w.Sgu.shape[1]) if w.Sgu is not None else (0, 0)
+        for name, t, shape in (("Wgu", w.Wgu, (2 * E, dff, dm)), ("Sgu", w.Sgu, (2 * ns, sdff, dm)), ("Sd", w.Sd, (ns, dm, sdff)),
+                               ("bias", bias, (E,)), ("x_scale", x_scale, (1,)), ("h_scale", h_scale, (1,))):
+            if t is None and name == "Sd" and ns:
+                raise ValueError("Fp4Layer: Sgu without Sd")
+            if t is not None and tuple(t.shape) != shape:
+                raise ValueError(f"Fp4Layer: {name} has shape {tuple(t.shape)}, needs {shape}")
         self.ctx, self.k, self.fmt, self.timer, self.max_tokens = ctx, k, fmt, timer, max_tokens
         self.x_scale, self.h_scale = x_scale, h_scale
-        self.E, self.d_model, self.d_ff = w.Wd.shape
+        self.E, self.d_model, self.d_ff = E, dm, dff
         self.gate = dict(score=score, bias=bias, n_groups=n_groups, top_groups=top_groups, group_rank=group_rank,
                          renormalise=renormalise, scale=scale)
         dev = self.dev = torch.device("cuda", ctx.device)
@@ -715,6 +723,9 @@ class Fp4Layer:
         ctx, t, n, E, k, fmt = self.ctx, self.timer, X.shape[0], self.E, self.k, self.fmt
         if n > self.max_tokens:
             raise ValueError(f"{n} tokens in a layer built for {self.max_tokens}")
+        for name, a, shape in (("X", X, (n, self.d_model)), ("logits", logits, (n, E)), ("Y", Y, (n, self.d_model))):
+            if tuple(a.shape) != shape:
+                raise ValueError(f"Fp4Layer.forward: {name} has shape {tuple(a.shape)}, needs {shape}")
         P = L.clha_packed_rows(n, k, E)
         dm, dff, xs, hs = self.d_model, self.d_ff, self.x_scale, self.h_scale
         ids, weights = self.ids[:n], self.weights[:n]

@@ -115,3 +115,24 @@ def test_gather_scratch():
             call(**kw)
     n = None
     assert L.load().clha_gather_scratch(n, n, 0, 0, 128, n, 1, 1, n, 128, n, n, n, 0) == L.ERR_INVALID_ARG
+
+
+def test_layer_shapes():
+    """Tensors of another shape than the layer's, although they hold enough elements."""
+    from types import SimpleNamespace
+    from post_quantization_expert_b200.pipeline import Fp4Layer, MoEWeights
+    b = lambda *s: t(*s, dtype=BF16)
+    ok = dict(Wgu=b(8, 128, 256), Wd=b(4, 256, 128), Sgu=b(4, 128, 256), Sd=b(2, 256, 128))
+    ctx = SimpleNamespace(device=0)
+    for kw, more in ((dict(Wgu=b(8, 256, 256)), {}), (dict(Wgu=b(8, 256, 128)), {}), (dict(Sgu=b(4, 128, 128)), {}),
+                     (dict(Sd=b(2, 128, 256)), {}), (dict(Sd=None), {}), ({}, dict(bias=t(5))), ({}, dict(x_scale=t(2))),
+                     ({}, dict(h_scale=torch.tensor(1.0)))):
+        with pytest.raises(ValueError, match=next(iter(kw or more))):
+            Fp4Layer(ctx, MoEWeights(**{**ok, **kw}), 2, 16, **more)
+    layer = object.__new__(Fp4Layer)
+    layer.ctx, layer.timer, layer.E, layer.k, layer.fmt, layer.d_model, layer.max_tokens = ctx, None, 4, 2, 0, 256, 16
+    X, lg, Y = t(3, 256), t(3, 4), t(3, 256)
+    for name, a in (("X", (t(3, 512), lg, Y)), ("logits", (X, t(3, 8), Y)), ("logits", (X, t(4, 4), Y)),
+                    ("Y", (X, lg, t(4, 256))), ("tokens", (t(17, 256), lg, Y))):
+        with pytest.raises(ValueError, match=name):
+            layer.forward(*a)
