@@ -237,7 +237,7 @@ __device__ __forceinline__ bool select_token(const GateArgs& p, const float (&l)
         const int j = lane + 32 * i;
         if (j < p.k) {
             float w = my_s[i];
-            if (p.renorm) w = sum > 0 ? w / sum : 1 / p.k;
+            if (p.renorm) w /= sum;                           // (above 1e-30)
             p.ids[t * p.k + j] = my_id[i];
             p.weights[t * p.k + j] = (float)(w * p.scale);
             atomicAdd(&hist[my_id[i]], 1);
