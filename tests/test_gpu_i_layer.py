@@ -1015,3 +1015,55 @@ def test_products_under_extreme_matrix_scales(ctx, x_scale, w_scale, top):
         check_act(h, x64 * both, w64[None], w64[None], None, K)
         assert (h[2] == 0).all()
     L.clha_check(ctx)
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("fmt", FMTS)
+def test_quantize_a_scale_for_each_expert(ctx, fmt, dtype):
+    """Weights of eight experts, each under its own matrix scale."""
+    E, rows, d = 8, 520, 384
+    x = (torch.randn((E, rows, d), generator=gen(31)) * torch.logspace(-3, 2, E)[:, None, None]).to(dtype)
+    g = torch.empty(E, device=DEV)
+    L.clha_fp4_tensor_scale(ctx, x.to(DEV), E, rows, d, FMT[fmt], g)
+    codes, scales = quantize(ctx, x.view(-1, d).to(DEV), fmt, g)
+    check_quantized(codes, scales, to64(x.view(-1, d)), fmt, np.repeat(to64(g), rows))
+    L.clha_check(ctx)
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("more", [0, 1, 5, 300])
+def test_products_of_more_tiles_than_the_sizes_tell(ctx, fmt, more):
+    """Each of 16 experts with 64 tokens in a call of their 2048 rows and `more`: the number of rows alone is that of far fewer
+    row tiles (2049 rows could hold one token), so that K is shared by a cluster."""
+    n, E, K, N = 64, 16, 4096, 128
+    _, seg, perm = route(n, E, E, 0)
+    rows, end = int(seg[E]) + more, int(seg[E])
+    assert end == 128 * E
+    x = torch.randn((rows, K), generator=gen(more)).to(BF16)
+    w = 0.05 * torch.randn((E * N, K), generator=gen(32))
+    (xq, xs, x64), (wq, ws, w64) = operand(ctx, x, fmt), operand(ctx, w, fmt)
+    w64, segd = w64.reshape(E, N, K), torch.from_numpy(seg).to(DEV)
+    y = torch.full((rows, N), 5.0, device=DEV)
+    L.clha_fp4_matmul(ctx, FMT[fmt], xq, xs, rows, K, wq, ws, N, y, seg=segd, E=E)
+    check_product(y[:end], O.expert_products(x64, w64, seg)[:end], O.expert_products(np.abs(x64), np.abs(w64), seg)[:end], K, F32)
+    h = torch.full((rows, N), 5.0, dtype=BF16, device=DEV)
+    L.clha_fp4_expert_act(ctx, FMT[fmt], xq, xs, rows, K, wq, ws, wq, ws, N, h, seg=segd, E=E)
+    check_act(h[:end], x64[:end], w64, w64, seg, K)
+    tokens = torch.from_numpy(perm[:end] >= 0)
+    for out in (y, h):
+        assert (out[end:] == 5.0).all() and (out[:end][~tokens] == 0).all()
+    L.clha_check(ctx)
+
+
+@pytest.mark.parametrize("n,N", [(20, 128), (64, 256), (4000, 1024)])
+def test_products_of_extreme_block_scales(ctx, n, N):
+    """Power-of-two block scales up to 2^127 that meet scales down to 2^-127: products of ordinary size."""
+    K = 256
+    up = torch.linspace(60, 125, K // 32).round().repeat_interleave(32)
+    x, w = torch.randn((n, K), generator=gen(n)).clamp(-3, 3), torch.randn((N, K), generator=gen(N)).clamp(-3, 3)
+    x, w = x * 2.0 ** up, w * 2.0 ** (-up)
+    (xq, xs, x64), (wq, ws, w64) = operand(ctx, x, "e8m0_32"), operand(ctx, w, "e8m0_32")
+    y = torch.empty((n, N), device=DEV)
+    L.clha_fp4_matmul(ctx, L.FP4_E8M0_32, xq, xs, n, K, wq, ws, N, y)
+    check_product(y, x64 @ w64.T, np.abs(x64) @ np.abs(w64).T, K, F32)
+    L.clha_check(ctx)
