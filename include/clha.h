@@ -144,7 +144,8 @@ CLHA_API clha_status clha_gather_noalloc(clha_ctx* ctx, const void* X, clha_dtyp
  * context's workspace, which grows, and moves, whenever a call on the context needs more of it: a
  * graph that captured this call keeps pointing at memory that the caller owns. perm is needed.
  * scratch: 4-byte aligned, clha_gather_scratch_bytes(n, E) or more (-1 for a bad E or an n
- * outside 0 .. 2^31 - 1; it grows with n); what it holds before and after does not matter. Nothing is allocated or synchronised. */
+ * outside 0 .. 2^31 - 1; it grows with n); what it holds before and after does not matter. Nothing is
+ * allocated or synchronised. */
 CLHA_API int64_t clha_gather_scratch_bytes(int64_t n, int E);
 CLHA_API clha_status clha_gather_scratch(clha_ctx* ctx, const void* X, clha_dtype dtype, int64_t n, int d,
                                          const int32_t* ids, int k, int E, void* X_packed, int64_t packed_rows,
@@ -359,7 +360,8 @@ CLHA_API clha_status clha_loss(clha_ctx* ctx, const void* W, clha_dtype dtype, c
 
 /* ------------------------------------------------------------------------------ 4-bit expert layer */
 
-/* The layer that the quantized experts run in, in microscaled 4-bit floating point:
+/* A layer whose experts run in microscaled 4-bit floating point (bf16 or f32 weights rounded to nearest; the codes
+ * of clha_quantize are another format and do not enter it):
  *   clha_route_gated -> clha_gather_scratch (perm only) -> clha_fp4_quantize (the routed rows)
  *   -> clha_fp4_expert_act -> clha_fp4_quantize -> clha_fp4_matmul -> clha_combine.
  * The pages stop at the quantized weights; these calls have no counterpart there. Nothing in them
@@ -389,7 +391,8 @@ typedef struct {
  * scores are all zero), counts [E] int32 is OVERWRITTEN with the tokens of each expert. Choices are
  * compared as float64 values, whatever the kernel computes them in; without a bias the logits decide,
  * unless groups are ranked by sums. A NaN or Inf logit or bias is recorded as CLHA_ERR_NONFINITE (and
- * counts as 0, so the ids stay in range). */
+ * counts as 0, so the ids stay in range): -Inf does not shut an expert out. A logit (without a bias) or
+ * a bias of float32's lowest value, -FLT_MAX, does, as long as k others are left in the groups that stay. */
 CLHA_API clha_status clha_route_gated(clha_ctx* ctx, const void* logits, clha_dtype dtype, int64_t n,
                                       const clha_route_params* params, const float* bias, int32_t* ids,
                                       float* weights, int32_t* counts);
@@ -412,7 +415,8 @@ CLHA_API int64_t clha_fp4_scale_bytes(clha_fp4_format format, int64_t rows, int 
 
 /* Matrix scales of `batch` matrices X [batch, rows, d] (f32 or bf16): scale [batch] (device float32) is
  * max|x| over the largest number that the format's blocks reach under scale 1 (6 for E8M0_32, 6 * 448 for
- * E4M3_16); 1 for a matrix of zeros. A NaN or Inf entry is recorded as CLHA_ERR_NONFINITE. */
+ * E4M3_16); 1 for a matrix of zeros, or where that quotient is below float32's range. A NaN or Inf entry is
+ * recorded as CLHA_ERR_NONFINITE. */
 CLHA_API clha_status clha_fp4_tensor_scale(clha_ctx* ctx, const void* X, clha_dtype dtype, int batch, int64_t rows,
                                            int d, clha_fp4_format format, float* scale);
 
@@ -434,9 +438,10 @@ CLHA_API clha_status clha_fp4_dequantize(clha_ctx* ctx, const uint8_t* codes, co
                                          void* X_hat, clha_dtype dtype);
 
 /* Y [rows, d_out] (f32 or bf16) = X W^T of operands in the same format: X [rows, d_in], W [E, d_out, d_in],
- * d_in and d_out multiples of 128, sums in float32 on the tensor cores. With seg NULL, E is 1; with seg,
- * rows follow its segments (rows >= seg[E]; segments start at multiples of 128) and expert e's rows meet W[e]:
- * rows of a segment behind its tokens are written as zero, rows from seg[E] on are left as they were.
+ * d_in and d_out multiples of 128, sums of q s products in float32 on the tensor cores (they have to stay in its
+ * range), which the matrix scales multiply. With seg NULL, E is 1; with seg, rows follow its segments (rows >=
+ * seg[E]; segments start at multiples of 128) and expert e's rows meet W[e]: rows of a segment behind its tokens
+ * are written as zero, rows from seg[E] on are left as they were.
  * x_scale: device float32 [1], w_scale [E], or NULL. rows * d_in and E * d_out * d_in below 2^37,
  * rows and E * d_out below 2^31. Y is 16-byte aligned. */
 CLHA_API clha_status clha_fp4_matmul(clha_ctx* ctx, clha_fp4_format format, const uint8_t* x_codes,
@@ -444,7 +449,8 @@ CLHA_API clha_status clha_fp4_matmul(clha_ctx* ctx, clha_fp4_format format, cons
                                      const int64_t* seg, int E, const uint8_t* w_codes, const uint8_t* w_scales,
                                      const float* w_scale, int d_out, void* Y, clha_dtype y_dtype);
 /* clha_expert_act on 4-bit operands: h [rows, d_ff] bf16 = SiLU(x Wg^T) * (x Wu^T), Wg and Wu [E, d_ff, d_model];
- * the float32 sums' product is rounded once. Arguments as in clha_fp4_matmul. */
+ * SiLU and the product are float32, off by at most (1.5 |gate sum| + 16) 2^-24 of their size, and h is rounded
+ * once. Arguments as in clha_fp4_matmul. */
 CLHA_API clha_status clha_fp4_expert_act(clha_ctx* ctx, clha_fp4_format format, const uint8_t* x_codes,
                                          const uint8_t* x_scales, const float* x_scale, int64_t rows, int d_model,
                                          const int64_t* seg, int E, const uint8_t* g_codes, const uint8_t* g_scales,

@@ -7,18 +7,24 @@
 //   q = x / (s g) rounded to the nearest e2m1 number, ties to the even code, saturating at +-6,
 // all of it decided as if in exact arithmetic. Divisions make that more than one float32 operation: the
 // quotient t is formed with reciprocals (relative error below 2^-21.9), t (1 - 2^-21) and t (1 + 2^-21)
-// are both rounded, and only where the two differ (about one block in 10^5) the lane decides again in
-// float64, where a quotient of a 24-bit by a 28-bit number cannot round onto a border that it is not on
-// (borders have at most 5 bits, so x and border * s * g differ by 2^-33 of their size or not at all).
+// are both rounded, and only where the two differ the lane decides again in float64, where a quotient of a 24-bit by
+// a 28-bit number cannot round onto a border that it is not on (borders have at most 5 bits, so x and border * s * g differ
+// by 2^-33 of their size or not at all). How often that is, counted over normal numbers: one block in 10^4 to 10^5 of
+// float32; of bfloat16, whose 8 bits put many values exactly on a border of e4m3 scales, one block in 6 without a matrix
+// scale and one in some 30 with one (none under power-of-two scales).
 // A power-of-two scale without g needs no quotient: x times a power of two is exact.
 //
 // Both kernels stream. Eight lanes take 128 columns, 16 a lane (32 bytes of bf16 in one access, 8 bytes of
 // codes), of the four rows r, r + 32, r + 64, r + 96 of a 128-row tile: four loads in flight a lane, and the
 // scales of four blocks of those rows are 16 consecutive bytes of the tiled layout (the lanes transpose 4 x 4
-// bytes by two exchanges and store 4 bytes each). A block is one lane (16) or two (32). Quantization is bound by
-// issue: 32768 tokens x 2048 into the segments of 64 experts, top 6, take 130 us (97 M warp instructions;
-// 8 columns a lane and a 64-bit division a step took 285 us, routed rows as they lie 142 us, runs of 512 columns
-// a unit 140 us). Decoding those to bf16 is bound by memory: 167 us, 93 % of the measured copy bandwidth.
+// bytes by two exchanges and store 4 bytes each). A block is one lane (16) or two (32). 32768 tokens x 2048 of bf16 into
+// the segments of 64 experts, top 6, under power-of-two scales take 130 us against 53 us for the bytes: 97 M warp
+// instructions in 64 % of the issue slots, half of the warps that an SM can hold, and each token decided once for each
+// of its experts (8 columns a lane and a 64-bit division a step took 285 us, routed rows as they lie 142 us, runs of 512
+// columns a unit 140 us). Every other variant does more for a block: float32 203 us; a matrix scale 302 us (a division of
+// the row's number and a reciprocal stand in the column loop); e4m3 scales 264 us over float32, and over bf16 1148 us, or
+// 433 us with a matrix scale: the float64 decisions above. Decoding to bf16 is bound by memory: 167 us, 93 % of the measured
+// copy bandwidth.
 #include "clha_internal.h"
 
 #include <cuda_fp16.h>
@@ -72,7 +78,7 @@ __device__ __forceinline__ float max_nan(float a, float b) {   // NaN if one is
     return r;
 }
 
-// ------------------------------------------------------------------ exact decisions, rarely taken
+// ------------------------------------------------------------------ exact decisions
 __device__ __noinline__ uint32_t e4m3_exact(double t) {       // t > 0
     if (t >= 448.0) return 0x7e;
     int e;

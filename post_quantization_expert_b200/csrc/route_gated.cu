@@ -253,7 +253,7 @@ __device__ __forceinline__ float finite_logit(const T* row, int e) {
 }
 
 // ------------------------------------------------------------------ the selection in float64
-// Taken by a warp for a token whose float32 choices leave a decision open: a token in thousands, but its
+// Taken by a warp for a token whose float32 choices leave a decision open (0 to 9 of 9973 tokens x 256 experts), but its
 // latency is the kernel's tail, so the doubles are compared as ordered 64-bit integers, whose warp-wide
 // maximum is two integer reductions (9973 x 256 experts with one such token: 24 us more as a selection by
 // exchanged doubles, 9 us more this way).
