@@ -8,7 +8,8 @@
 //   2. one block: per expert, exclusive scan of the block histograms; segment
 //      starts = exclusive scan of counts rounded up to 128                       (scan)
 //   3. per block: each (token, slot) finds its rank among earlier tokens of the
-//      block routed to the same expert and writes its token index to perm       (scatter)
+//      block routed to the same expert and writes its token index to perm       (scatter;
+//      with more than 48 slots a token, a thread for each expert does it)
 //   4. one warp per packed row: 16-byte vector copy of the token's row, or zeros (copy)
 #include "clha_internal.h"
 
@@ -84,6 +85,24 @@ __global__ void __launch_bounds__(kTB) gather_scatter(const int32_t* __restrict_
     }
 }
 
+// The same for lists of choices that do not fit shared memory (k > 48): a thread an expert walks the block's list, which the
+// threads of a warp read together.
+__global__ void __launch_bounds__(1024) gather_scatter_many(const int32_t* __restrict__ ids, int64_t n, int k, int E,
+                                                            const int* __restrict__ H, int32_t* __restrict__ perm) {
+    const int64_t t0 = (int64_t)blockIdx.x * kTB;
+    const int nt = (n - t0 < kTB) ? (int)(n - t0) : kTB;
+    for (int e = threadIdx.x; e < E; e += blockDim.x) {
+        const int32_t* list = ids + t0 * k;
+        int64_t pos = H[(size_t)blockIdx.x * E + e];
+        for (int i = 0; i < nt; ++i, list += k) {
+            int times = 0;   // an expert named twice takes two rows, of which the second stays empty
+            for (int j = 0; j < k; ++j) times += __ldg(list + j) == e;
+            if (times) perm[pos] = (int32_t)(t0 + i);
+            pos += times;
+        }
+    }
+}
+
 __global__ void gather_copy(const uint4* __restrict__ X, int64_t row_vecs, const int32_t* __restrict__ perm,
                             const int64_t* __restrict__ seg, int E, int64_t packed_rows, uint4* __restrict__ Xp) {
     const int lane = threadIdx.x & 31;
@@ -128,7 +147,10 @@ cudaError_t launch_gather(cudaStream_t s, const void* X, int esize, int64_t n, i
     clha_note_launches(1);
     gather_scan<<<1, 1024, 0, s>>>(H, (int)nblk, E, seg);
     clha_note_launches(1);
-    gather_scatter<<<(unsigned)nblk, kTB, kTB * k * sizeof(int), s>>>(ids, n, k, E, H, pm);
+    if (k <= 48)   // 48 KB of choices a block
+        gather_scatter<<<(unsigned)nblk, kTB, kTB * k * sizeof(int), s>>>(ids, n, k, E, H, pm);
+    else
+        gather_scatter_many<<<(unsigned)nblk, (E + 31) / 32 * 32, 0, s>>>(ids, n, k, E, H, pm);
     clha_note_launches(1);
     if (!X_packed) return cudaGetLastError();   // the permutation alone: the rows are read where they are
     int64_t row_vecs = (int64_t)d * esize / 16;

@@ -1067,3 +1067,27 @@ def test_products_of_extreme_block_scales(ctx, n, N):
     L.clha_fp4_matmul(ctx, L.FP4_E8M0_32, xq, xs, n, K, wq, ws, N, y)
     check_product(y, x64 @ w64.T, np.abs(x64) @ np.abs(w64).T, K, F32)
     L.clha_check(ctx)
+
+
+@pytest.mark.parametrize("n,E,k", [(700, 64, 48), (700, 64, 49), (300, 256, 130), (257, 1024, 1024)])
+def test_gather_of_many_choices(ctx, n, E, k):
+    """More choices a token than fit a block's shared memory; one token names an expert twice, another one outside."""
+    ids, _, _ = route(n, E, k, n)
+    ids[5, 1], ids[n - 1, 0] = ids[5, 0], E
+    counts = np.bincount(ids[ids < E], minlength=E)
+    starts = np.concatenate([[0], np.cumsum((counts + 127) // 128 * 128)])
+    P = L.clha_packed_rows(n, k, E)
+    want = np.full(P, -1, np.int32)
+    for e in range(E):                     # a token's row where its first choice of e comes in the count
+        at = starts[e]
+        for t, c in enumerate((ids == e).sum(1)):
+            if c:
+                want[at] = t
+                at += c
+    perm, seg = torch.zeros(P, dtype=torch.int32, device=DEV), torch.zeros(2 * E + 1, dtype=torch.int64, device=DEV)
+    L.clha_gather(ctx, torch.zeros((n, 128), device=DEV), n, 128, torch.from_numpy(ids).to(DEV), k, E, None, P, seg, perm)
+    np.testing.assert_array_equal(seg.cpu().numpy(), np.concatenate([starts, counts]))
+    np.testing.assert_array_equal(perm.cpu().numpy(), want)
+    with pytest.raises(L.ClhaError) as ei:
+        L.clha_check(ctx)
+    assert ei.value.status == L.ERR_INVALID_ARG
