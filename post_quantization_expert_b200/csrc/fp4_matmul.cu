@@ -3,10 +3,10 @@
 //
 // tcgen05.mma multiplies e2m1 values and applies both operands' block scales, accumulating in float32;
 // the matrix scales multiply the finished sums in the epilogue. Two kernels: pairs of SMs on large tiles (further
-// down), bound by the tensor pipe under the power limit (28672 -> 8192 on 16384 tokens: 1.6 to 1.7 ms, 4.5 to 4.8 PFLOP/s), and
-// one for few rows, bound by reading W (1 token of the same: 25 us, the same weights again or four sets in turn, 80 % of
-// the measured copy bandwidth); launch_product chooses. Segments start at multiples of 128, so a tile never mixes experts. Rows of a segment
-// behind its tokens are written as zero; rows behind the last segment are not touched.
+// down), bound by the tensor pipe under the power limit (28672 -> 8192 on 16384 tokens: 1.6 to 1.7 ms, 4.5 to 4.8
+// PFLOP/s), and one for few rows, bound by reading W (1 token of the same: 25 us, the same weights again or four sets in
+// turn, 80 % of the measured copy bandwidth); launch_product chooses. Segments start at multiples of 128, so a tile never
+// mixes experts. Rows of a segment behind its tokens are written as zero; rows behind the last segment are not touched.
 //
 // Few rows. The tensor core's 128-row operand is W (for gate and up a block of each), its other operand the
 // tile's rows of X, as many as hold tokens, in steps of 16: a decoding step pays for 16 rows, not for 128,

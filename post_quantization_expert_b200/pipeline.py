@@ -719,7 +719,8 @@ class Fp4Layer:
 
     def forward(self, X: torch.Tensor, logits: torch.Tensor, Y: torch.Tensor):
         """Y [n, d_model] (f32 or bf16) of the tokens X [n, d_model] (f32 or bf16) with router logits [n, E];
-        n <= max_tokens. Returns Y."""
+        n <= max_tokens. Returns Y. All three are used on the context's stream, in the order of its queue: a caller on
+        another stream orders the two, and keeps X and the logits until the call has run."""
         ctx, t, n, E, k, fmt = self.ctx, self.timer, X.shape[0], self.E, self.k, self.fmt
         if n > self.max_tokens:
             raise ValueError(f"{n} tokens in a layer built for {self.max_tokens}")
